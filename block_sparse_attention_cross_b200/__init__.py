@@ -35,6 +35,7 @@ __all__ = [
     "compile", "compile_size", "selftest_wait_timeout", "min_votes_for", "topk_count", "launch_count",
     "default_scale", "CalibattError", "BF16", "FP32", "SELECT_TOPK", "SELECT_ENERGY",
     "DEDUP_NONE", "DEDUP_HASH", "DEDUP_HASH_WEAK", "load",
+    "AttnSpans", "attn_spans", "relative_buckets", "score_attn_fwd", "score_attn_bwd",
     "save_state", "load_state", "save_calibration", "load_calibration", "save_masks", "load_masks",
     "save_blocklist", "load_blocklist",
 ]
@@ -729,3 +730,4 @@ def selftest_wait_timeout(limit_ns=10_000_000, device=None):
 
 from .dictionary import (load_blocklist, load_calibration, load_masks, load_state, save_blocklist,  # noqa: E402
                          save_calibration, save_masks, save_state)
+from .score import AttnSpans, attn_spans, relative_buckets, score_attn_bwd, score_attn_fwd  # noqa: E402

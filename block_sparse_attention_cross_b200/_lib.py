@@ -84,6 +84,19 @@ EXPORTS = {
     "calibatt_spatial_similarity_workspace_size": (c_int, [c_int, c_int, POINTER(c_size_t)]),
     "calibatt_spatial_similarity": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
                                             c_int, c_float, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "calibatt_relative_buckets": (c_int, [c_int, c_int, c_int, c_void_p]),
+    "calibatt_attn_spans": (c_int, [c_int, c_int, c_int, c_int, c_void_p, c_int, c_void_p, c_void_p, c_void_p,
+                                    c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "calibatt_score_attn_fwd_workspace_size": (c_int, [c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                                       POINTER(c_size_t)]),
+    "calibatt_score_attn_fwd": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                        c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
+                                        c_void_p]),
+    "calibatt_score_attn_bwd_workspace_size": (c_int, [c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                                       POINTER(c_size_t)]),
+    "calibatt_score_attn_bwd": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                                        c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int, c_int, c_int,
+                                        c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "calibatt_repetition_flags": (c_int, [c_void_p, c_int, c_int, c_float, c_void_p, c_void_p, c_void_p]),
 }
 
@@ -98,6 +111,27 @@ class Blocklist(ctypes.Structure):
         ("csr_row_ptr", c_void_p), ("csr_col", c_void_p),
         ("n_pat", c_int32), ("nnz_pat", c_int32), ("nnz", c_int64),
     ]
+
+
+class Tensor4(ctypes.Structure):
+    """Mirror of ``calibatt_tensor4``."""
+
+    _fields_ = [("ptr", c_void_p), ("stride_b", c_int64), ("stride_h", c_int64), ("stride_n", c_int64)]
+
+
+class Spans(ctypes.Structure):
+    """Mirror of ``calibatt_spans``."""
+
+    _fields_ = [("B", c_int32), ("Nq", c_int32), ("Nk", c_int32),
+                ("row", c_void_p), ("tile", c_void_p), ("q_start", c_void_p)]
+
+
+class Score(ctypes.Structure):
+    """Mirror of ``calibatt_score``."""
+
+    _fields_ = [("scale", c_float), ("cap", c_float), ("slopes", c_void_p), ("table", c_void_p),
+                ("buckets", c_void_p), ("n_buckets", c_int32), ("max_distance", c_int32),
+                ("mask", c_void_p), ("n_maps", c_int32), ("map_offset", c_int32)]
 
 
 _lib = None

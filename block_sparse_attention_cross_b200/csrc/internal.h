@@ -74,6 +74,50 @@ int launch_simt_fwd(const void* q, const void* k, const void* v, void* o, int d,
                     cudaStream_t s);
 int launch_simt_energy(const void* q, const void* k, int d, const SimtArgs& a, cudaStream_t s);
 
+// Kernel arguments of the score-modified attention (score_*.cu).
+struct Tensor4 {            // [B, heads, N, d], d contiguous; strides in elements
+  void* p;
+  long long sb, sh, sn;
+};
+struct ScoreArgs {
+  int B, H, Hkv, G;         // G = H / Hkv query heads per key head
+  int Nq, Nk, nqb, nkb;     // nqb, nkb: 128-row query tiles, 128-key tiles
+  float scale, cap;         // cap = 0: scores are not capped
+  const float* slopes;      // [H] or nullptr
+  const void* table;        // [H, n_buckets] of the inputs' type or nullptr
+  const int32_t* buckets;   // [2 R + 1]
+  int n_buckets, R;
+  const uint8_t* mask;      // [maps, nqb, nkb] kept 128 x 128 blocks or nullptr
+  int map_offset;
+  const int2* row;          // [B, Nq] visible keys [x, y) of every query row
+  const int4* tile;         // [B, nqb] min x, max y, max x, min y over a tile's rows
+  const int32_t* q_start;   // [B] key position of query row 0
+  Tensor4 q, k, v, o, dout, dq, dk, dv;
+  float* lse;               // [B, H, Nq] (forward: written, may be nullptr; backward: read)
+  void* dtable;             // [H, n_buckets] or nullptr
+  // workspace
+  int splits, packed;       // forward: splits of the key axis; packed: the G heads of a key head share a tile
+  float* part_o;            // [B, H, Nq, splits, d]
+  float* part_lse;          // [B, H, Nq, splits]
+  float* row_lse;           // backward: [B, H, 128 nqb] LSE, +inf where a row sees nothing
+  float* row_d;             // backward: [B, H, 128 nqb] sum over d of dO O
+  float* part_table;        // backward: [B, H, table tiles, n_buckets]
+  int table_tiles;          // query tiles per head that write part_table
+  int32_t* status;
+  unsigned long long spin_ns;
+};
+
+// score_simt.cu (fp32, FFMA)
+int launch_score_fwd_simt(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
+int launch_score_bwd_simt(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
+// score_plan.cu
+int launch_attn_spans(int B, int Nq, int Nk, int causal, const int32_t* docs, int n_docs, const int32_t* prefix,
+                      const int32_t* kv_len, const int32_t* q_len, const int32_t* q_start, int2* row, int4* tile,
+                      int32_t* q_start_out, cudaStream_t s);
+// score_rows.cu: per-row terms of the backward pass, the sum of the table's partial gradients
+int launch_score_rows(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
+int launch_score_table_sum(const ScoreArgs& a, int dtype, cudaStream_t s);
+
 // select_vote.cu
 int launch_select_vote(const float* energy, int rows, int nkb, int mode, int topk, double eps,
                        int32_t* votes, float* esum, cudaStream_t s);

@@ -1,0 +1,98 @@
+// score_rows.cu -- the small kernels around the score-modified attention's
+// backward pass.
+#include "score_common.cuh"
+
+namespace calibatt {
+namespace {
+
+// D_i = sum over d of dO_i O_i, and the row's LSE as the backward kernels read
+// it: +inf where the row sees nothing (every probability becomes 0), NaN where
+// D is not finite (so that a row with a non-finite dO or O marks every
+// gradient it enters).  One warp a row: reads dO and O once, DRAM-bound.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) k_score_rows(const ScoreArgs a) {
+  const long long rows = 128ll * a.nqb;
+  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (w >= rows * a.B * a.H) return;
+  const int lane = threadIdx.x & 31;
+  const int bh = static_cast<int>(w / rows), i = static_cast<int>(w % rows);
+  const int b = bh / a.H, h = bh % a.H;
+  float sum = 0.f, lse = INFINITY;
+  const int2 r = score_row(a, b, i);
+  if (r.x < r.y) {
+    const T* po = reinterpret_cast<const T*>(a.o.p) + b * a.o.sb + h * a.o.sh + i * a.o.sn;
+    const T* pd = reinterpret_cast<const T*>(a.dout.p) + b * a.dout.sb + h * a.dout.sh + i * a.dout.sn;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int x = lane * 2; x < D; x += 64) {
+        const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(po + x));
+        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(pd + x));
+        sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
+      }
+    } else {
+#pragma unroll
+      for (int x = lane; x < D; x += 32) sum = fmaf(po[x], pd[x], sum);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    lse = a.lse[static_cast<size_t>(bh) * a.Nq + i];
+    if (lse == -INFINITY) { lse = INFINITY; sum = 0.f; }
+    else if (!isfinite(sum)) lse = NAN;
+  }
+  if (lane == 0) {
+    a.row_lse[w] = lse;
+    a.row_d[w] = sum;
+  }
+}
+
+// Gradient of the bias table: the partial sums of every (batch entry, query
+// tile) of a head, added in a fixed order in double.  One CTA per (head,
+// bucket).
+template <typename T>
+__global__ void __launch_bounds__(128) k_score_table_sum(const ScoreArgs a) {
+  const int h = blockIdx.y, n = blockIdx.x;
+  const int tiles = a.B * a.table_tiles;
+  double s = 0.0;
+  for (int t = threadIdx.x; t < tiles; t += 128) {
+    const int b = t / a.table_tiles, q = t % a.table_tiles;
+    s += a.part_table[((static_cast<size_t>(b) * a.H + h) * a.table_tiles + q) * a.n_buckets + n];
+  }
+  __shared__ double red[128];
+  red[threadIdx.x] = s;
+  __syncthreads();
+  for (int m = 64; m > 0; m >>= 1) {
+    if (threadIdx.x < m) red[threadIdx.x] += red[threadIdx.x + m];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const float r = static_cast<float>(red[0]);
+    if constexpr (sizeof(T) == 2) reinterpret_cast<__nv_bfloat16*>(a.dtable)[h * a.n_buckets + n] = __float2bfloat16(r);
+    else reinterpret_cast<float*>(a.dtable)[h * a.n_buckets + n] = r;
+  }
+}
+
+}  // namespace
+
+int launch_score_rows(const ScoreArgs& a, int d, int dtype, cudaStream_t s) {
+  const long long rows = 128ll * a.nqb * a.B * a.H;
+  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  if (dtype == CALIBATT_BF16) {
+    if (d == 128) k_score_rows<__nv_bfloat16, 128><<<grid, 256, 0, s>>>(a);
+    else k_score_rows<__nv_bfloat16, 64><<<grid, 256, 0, s>>>(a);
+  } else {
+    if (d == 128) k_score_rows<float, 128><<<grid, 256, 0, s>>>(a);
+    else k_score_rows<float, 64><<<grid, 256, 0, s>>>(a);
+  }
+  count_launch();
+  return check_launch("k_score_rows");
+}
+
+int launch_score_table_sum(const ScoreArgs& a, int dtype, cudaStream_t s) {
+  const dim3 grid(a.n_buckets, a.H);
+  if (dtype == CALIBATT_BF16) k_score_table_sum<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
+  else k_score_table_sum<float><<<grid, 128, 0, s>>>(a);
+  count_launch();
+  return check_launch("k_score_table_sum");
+}
+
+}  // namespace calibatt

@@ -1,0 +1,263 @@
+"""Score-modified attention: binding of ``calibatt_attn_spans``,
+``calibatt_score_attn_fwd`` and ``calibatt_score_attn_bwd``.
+
+Attention whose scores are capped by a tanh, biased by distance (a slope a
+head, a learned table of buckets) and restricted to documents, a prefix or
+lengths, on the kept blocks of a calibrated mask where one is given; with its
+gradients, the table's included.  The definition stands in
+``include/calibatt.h``.  As everywhere in this package the module checks and
+marshals arguments, allocates outputs and workspace and passes the stream.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from dataclasses import dataclass
+
+import numpy as np
+import torch
+
+from . import _lib
+from ._lib import BF16, FP32, check, load
+
+_DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
+
+
+def _ptr(t):
+    return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _stream(device):
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+@dataclass
+class AttnSpans:
+    """Visible keys of every query row (see ``calibatt_spans``), from :func:`attn_spans`."""
+
+    B: int
+    Nq: int
+    Nk: int
+    row: torch.Tensor       # [B, Nq, 2] int32: first visible key, one past the last
+    tile: torch.Tensor      # [B, ceil(Nq / 128), 4] int32: ranges of 128-row tiles
+    q_start: torch.Tensor   # [B] int32: key position of query row 0
+
+    def as_struct(self):
+        s = _lib.Spans()
+        s.B, s.Nq, s.Nk = self.B, self.Nq, self.Nk
+        s.row, s.tile, s.q_start = self.row.data_ptr(), self.tile.data_ptr(), self.q_start.data_ptr()
+        return s
+
+
+def _ints(name, x, shape, device):
+    """int32 CUDA tensor of ``shape`` (None: not given); lists and host tensors are copied to the device."""
+    if x is None:
+        return None
+    t = torch.as_tensor(x)
+    if t.is_floating_point() or t.is_complex() or t.dtype == torch.bool:
+        raise ValueError(f"{name} must hold integers")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.is_cuda and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.to(device=device, dtype=torch.int32).contiguous()
+
+
+def attn_spans(B, Nq, Nk, *, causal=False, docs=None, prefix=None, kv_len=None, q_len=None, q_start=None,
+               device="cuda"):
+    """The keys every query row sees (``calibatt_attn_spans``), as one interval a row.
+
+    Row i of batch entry b stands at key position ``q_start[b] + i`` (default
+    0; a single new token: its position).  It sees the ``kv_len[b]`` keys of
+    its batch entry, or with ``docs`` ([B, n_docs + 1] ascending bounds of
+    documents packed back to back) those of its document; with ``causal`` only
+    keys up to its own position and the first ``prefix[b, m]`` keys of its
+    document ([B, n_docs], or [B] without documents).  Rows from ``q_len[b]``
+    on see nothing.  Make it once per batch layout; every layer's calls share it.
+    """
+    B, Nq, Nk = int(B), int(Nq), int(Nk)
+    if B <= 0 or Nq <= 0 or Nk <= 0:
+        raise ValueError("B, Nq and Nk must be positive")
+    device = torch.device(device)
+    if device.type != "cuda":
+        raise ValueError("the spans are computed on a CUDA device")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    if prefix is not None and not causal:
+        raise ValueError("a prefix needs causal=True")
+    n_docs = 0
+    if docs is not None:
+        docs = torch.as_tensor(docs)
+        if docs.dim() != 2 or docs.shape[0] != B or docs.shape[1] < 2:
+            raise ValueError(f"docs must be [B, n_docs + 1] with B = {B}")
+        n_docs = docs.shape[1] - 1
+        docs = _ints("docs", docs, (B, n_docs + 1), device)
+    if prefix is not None:
+        prefix = torch.as_tensor(prefix)
+        if n_docs == 0 and prefix.dim() == 1:
+            prefix = prefix[:, None]
+        prefix = _ints("prefix", prefix, (B, max(n_docs, 1)), device)
+    kv_len = _ints("kv_len", kv_len, (B,), device)
+    q_len = _ints("q_len", q_len, (B,), device)
+    q_start = _ints("q_start", q_start, (B,), device)
+    sp = AttnSpans(B, Nq, Nk, torch.empty((B, Nq, 2), dtype=torch.int32, device=device),
+                   torch.empty((B, -(-Nq // 128), 4), dtype=torch.int32, device=device),
+                   torch.empty(B, dtype=torch.int32, device=device))
+    with torch.cuda.device(device):
+        check(load().calibatt_attn_spans(B, Nq, Nk, int(bool(causal)), _ptr(docs), n_docs, _ptr(prefix), _ptr(kv_len),
+                                         _ptr(q_len), _ptr(q_start), _ptr(sp.row), _ptr(sp.tile), _ptr(sp.q_start),
+                                         _stream(device)))
+    return sp
+
+
+def relative_buckets(n_buckets, max_distance, bidirectional=True, device="cuda"):
+    """Bucket map [2 max_distance + 1] int32 of a learned relative bias (``calibatt_relative_buckets``):
+    own buckets near zero, logarithmic ones out to ``max_distance``, farther offsets in the last."""
+    n = max(int(max_distance), 0)
+    out = np.zeros(2 * n + 1, dtype=np.int32)
+    check(load().calibatt_relative_buckets(int(n_buckets), int(max_distance), int(bool(bidirectional)),
+                                           out.ctypes.data_as(ctypes.c_void_p)))
+    return torch.from_numpy(out).to(device)
+
+
+def _tensor4(name, t, shape, dtype, device):
+    """Checks a [B, heads, N, d] tensor and returns its ``calibatt_tensor4``."""
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    st = t.stride()
+    if st[3] != 1 or any(n > 1 and (s <= 0 or s * t.element_size() % 16) for n, s in zip(shape[:3], st[:3])):
+        raise ValueError(f"{name}: the last dimension must be contiguous and the others' strides positive multiples "
+                         f"of 16 bytes, got strides {st} (an expanded tensor needs .contiguous())")
+    return _lib.Tensor4(t.data_ptr(), st[0], st[1], st[2])
+
+
+def _flat(name, t, shape, dtype, device):
+    """Checks a contiguous operand (None: not given)."""
+    if t is None:
+        return
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+
+
+def _prepare(q, k, v, spans, scale, cap, slopes, table, buckets, mask, map_offset, status):
+    """Argument checks shared by the forward and the backward: sizes, the score struct and its operands."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, H, Nq, d] and k, v [B, Hkv, Nk, d]")
+    if q.dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {q.dtype}: use torch.bfloat16 or torch.float32")
+    B, H, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    if Hkv == 0 or H % Hkv:
+        raise ValueError(f"H = {H} must be a multiple of Hkv = {Hkv}")
+    if not isinstance(spans, AttnSpans):
+        raise TypeError("spans must come from attn_spans")
+    if (spans.B, spans.Nq, spans.Nk) != (B, Nq, Nk):
+        raise ValueError(f"spans of B, Nq, Nk = {spans.B, spans.Nq, spans.Nk} do not match {B, Nq, Nk}")
+    dev = q.device
+    _flat("spans.row", spans.row, (B, Nq, 2), torch.int32, dev)
+    _flat("spans.tile", spans.tile, (B, -(-Nq // 128), 4), torch.int32, dev)
+    _flat("spans.q_start", spans.q_start, (B,), torch.int32, dev)
+    if (table is None) != (buckets is None):
+        raise ValueError("table and buckets come together")
+    sc = _lib.Score()
+    sc.scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    sc.cap = float(cap)
+    _flat("slopes", slopes, (H,), torch.float32, dev)
+    sc.slopes = None if slopes is None else slopes.data_ptr()
+    if table is not None:
+        if table.dim() != 2 or buckets.dim() != 1 or buckets.numel() % 2 == 0:
+            raise ValueError("table must be [H, n_buckets] and buckets [2 max_distance + 1]")
+        _flat("table", table, (H, table.shape[1]), q.dtype, dev)
+        _flat("buckets", buckets, tuple(buckets.shape), torch.int32, dev)
+        sc.table, sc.buckets = table.data_ptr(), buckets.data_ptr()
+        sc.n_buckets, sc.max_distance = table.shape[1], buckets.numel() // 2
+    if mask is not None:
+        if mask.dim() != 3:
+            raise ValueError("mask must be uint8 [n_maps, nqb, nkb]")
+        _flat("mask", mask, (mask.shape[0], -(-Nq // 128), -(-Nk // 128)), torch.uint8, dev)
+        sc.mask, sc.n_maps, sc.map_offset = mask.data_ptr(), mask.shape[0], int(map_offset)
+    if status is not None:
+        if status.dtype != torch.int32 or status.numel() < 1:
+            raise ValueError("status must be an int32 tensor with at least one element")
+        _flat("status", status, tuple(status.shape), torch.int32, dev)
+    return (B, H, Hkv, Nq, Nk, d), sc
+
+
+def _workspace(nbytes, device):
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def score_attn_fwd(q, k, v, spans: AttnSpans, *, scale=None, cap=0.0, slopes=None, table=None, buckets=None, mask=None,
+                   map_offset=0, return_lse=False, out=None, lse=None, status=None):
+    """Score-modified attention forward (``calibatt_score_attn_fwd``).
+
+    q: [B, H, Nq, d]; k, v: [B, Hkv, Nk, d], bf16 or fp32 on the GPU, H a
+    multiple of Hkv, d 64 or 128, any strides with the last dimension
+    contiguous and 16-byte aligned rows.  ``spans``: the keys every row sees
+    (:func:`attn_spans`).  Scores: scale q.k (scale 1/sqrt(d) when None),
+    capped to cap tanh(s / cap) when ``cap`` > 0, minus ``slopes``[h] |j - p|
+    ([H] float32), plus ``table``[h, buckets[j - p]] ([H, n_buckets] of q's
+    type; ``buckets`` int32 [2 max_distance + 1], e.g. from
+    :func:`relative_buckets`).  ``mask``: uint8 [n_maps, nqb, nkb] kept 128 x
+    128 blocks (as :func:`calibrate` returns), head h uses map ``map_offset``
+    + h.  Returns O (laid out like q) and, with ``return_lse``, LSE [B, H, Nq].
+    """
+    (B, H, Hkv, Nq, Nk, d), sc = _prepare(q, k, v, spans, scale, cap, slopes, table, buckets, mask, map_offset, status)
+    dev, dt = q.device, q.dtype
+    tq = _tensor4("q", q, (B, H, Nq, d), dt, dev)
+    tk = _tensor4("k", k, (B, Hkv, Nk, d), dt, dev)
+    tv = _tensor4("v", v, (B, Hkv, Nk, d), dt, dev)
+    if out is None:
+        out = torch.empty_like(q)
+    to = _tensor4("out", out, (B, H, Nq, d), dt, dev)
+    if return_lse and lse is None:
+        lse = torch.empty((B, H, Nq), device=dev, dtype=torch.float32)
+    _flat("lse", lse, (B, H, Nq), torch.float32, dev)
+    n = ctypes.c_size_t(0)
+    sizes = (B, H, Hkv, Nq, Nk, d, _DTYPES[dt])
+    check(load().calibatt_score_attn_fwd_workspace_size(*sizes, ctypes.byref(n)))
+    sp = spans.as_struct()
+    with torch.cuda.device(dev):
+        ws = _workspace(n.value, dev)
+        check(load().calibatt_score_attn_fwd(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), ctypes.byref(to),
+                                             _ptr(lse), *sizes, ctypes.byref(sp), ctypes.byref(sc), _ptr(ws), n.value,
+                                             _ptr(status), _stream(dev)))
+    return (out, lse) if return_lse else out
+
+
+def score_attn_bwd(dout, q, k, v, o, lse, spans: AttnSpans, *, scale=None, cap=0.0, slopes=None, table=None,
+                   buckets=None, mask=None, map_offset=0, status=None):
+    """Gradients of :func:`score_attn_fwd` (``calibatt_score_attn_bwd``).
+
+    ``dout``: gradient of O; ``o``, ``lse``: the forward's results; the other
+    arguments as given to the forward.  Returns (dq, dk, dv), laid out like q,
+    k and v, and the table's gradient [H, n_buckets] as fourth where a table
+    is given.  Deterministic.
+    """
+    (B, H, Hkv, Nq, Nk, d), sc = _prepare(q, k, v, spans, scale, cap, slopes, table, buckets, mask, map_offset, status)
+    dev, dt = q.device, q.dtype
+    qs, ks = (B, H, Nq, d), (B, Hkv, Nk, d)
+    ins = [_tensor4("dout", dout, qs, dt, dev), _tensor4("q", q, qs, dt, dev), _tensor4("k", k, ks, dt, dev),
+           _tensor4("v", v, ks, dt, dev), _tensor4("o", o, qs, dt, dev)]
+    _flat("lse", lse, (B, H, Nq), torch.float32, dev)
+    if lse is None:
+        raise ValueError("lse must be the forward's (return_lse=True)")
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    outs = [_tensor4("dq", dq, qs, dt, dev), _tensor4("dk", dk, ks, dt, dev), _tensor4("dv", dv, ks, dt, dev)]
+    dtable = None if table is None else torch.empty_like(table)
+    n = ctypes.c_size_t(0)
+    sizes = (B, H, Hkv, Nq, Nk, d, _DTYPES[dt])
+    check(load().calibatt_score_attn_bwd_workspace_size(*sizes, 0 if table is None else table.shape[1],
+                                                        ctypes.byref(n)))
+    sp = spans.as_struct()
+    with torch.cuda.device(dev):
+        ws = _workspace(n.value, dev)
+        check(load().calibatt_score_attn_bwd(*(ctypes.byref(t) for t in ins), _ptr(lse),
+                                             *(ctypes.byref(t) for t in outs), _ptr(dtable), *sizes, ctypes.byref(sp),
+                                             ctypes.byref(sc), _ptr(ws), n.value, _ptr(status), _stream(dev)))
+    return (dq, dk, dv) if table is None else (dq, dk, dv, dtable)

@@ -593,6 +593,147 @@ int calibatt_blocklist_kept(const calibatt_blocklist* bl, int map_offset, int n_
                             size_t workspace_bytes, calibatt_stream_t stream);
 
 /*
+ * Score-modified attention: forward and backward
+ * -----------------------------------------------
+ * Attention for models whose scores are capped, biased by distance (a fixed
+ * slope a head, a learned table of buckets, or both) or restricted to
+ * documents, prefixes and lengths, optionally on the kept blocks of a
+ * calibrated mask.  The paper has no counterpart; the definition is
+ *     p     = q_start[b] + i                     key position of query row i
+ *     s_ij  = scale q_i.k_j
+ *     c_ij  = cap tanh(s_ij / cap)               (s_ij when cap = 0)
+ *     z_ij  = c_ij - slopes[h] |j - p| + table[h, buckets[clip(j - p, -R, R) + R]]
+ *     O_i   = sum_j P_ij v_j,  P_ij = exp(z_ij - LSE_i),  LSE_i = ln sum_j exp z_ij
+ * over the keys j that row i sees: those of its interval (calibatt_attn_spans)
+ * in kept blocks.  A row that sees nothing gets O_i = 0, LSE_i = -inf and no
+ * gradient.  With D_i = sum_d dO O and dZ_ij = P_ij (dO_i.v_j - D_i):
+ *     dV_j = sum_i P_ij dO_i,  dTable[h, n] = sum over b and the pairs of bucket n of dZ_ij,
+ *     dQ_i = scale sum_j dZ_ij (1 - (c_ij/cap)^2) k_j,  dK_j = scale sum_i dZ_ij (1 - (c_ij/cap)^2) q_i.
+ * Query head h reads key head h / (H / Hkv); dK and dV add up the query heads
+ * that share a key head.
+ *
+ * Unlike the calls above, lengths need no padding and tensors may be strided:
+ * a calibatt_tensor4 is [B, heads, N, d] with d contiguous, a 16-byte aligned
+ * base and strides (in elements) that are positive multiples of 16 bytes;
+ * strides of dimensions of one entry are not read.  Outputs may not overlap.
+ *
+ * Values of masked places do not matter, NaN and infinities included: a key
+ * (query) row reaches only the rows that see it (that it sees).  A row that
+ * sees a key with a non-finite value v_j in a tile that the mask cuts becomes
+ * NaN as a whole.
+ */
+typedef struct calibatt_tensor4 {
+  void* ptr;
+  int64_t stride_b, stride_h, stride_n;
+} calibatt_tensor4;
+
+/* Visible keys of every query row (calibatt_attn_spans), device memory. */
+typedef struct calibatt_spans {
+  int32_t B, Nq, Nk;
+  const int32_t* row;     /* [B, Nq, 2] first visible key, one past the last (equal: none); 8-byte aligned      */
+  const int32_t* tile;    /* [B, ceil(Nq / 128), 4] over a tile's rows: the least first, greatest end, greatest
+                             first and least end; 16-byte aligned                                              */
+  const int32_t* q_start; /* [B] key position of query row 0                                                    */
+} calibatt_spans;
+
+/* The score function. */
+typedef struct calibatt_score {
+  float scale;            /* finite, > 0                                                                        */
+  float cap;              /* finite, > 0; 0: no cap                                                             */
+  const float* slopes;    /* [H] float32 device or NULL                                                         */
+  const void* table;      /* [H, n_buckets] of the inputs' type, device, or NULL                                */
+  const int32_t* buckets; /* [2 max_distance + 1] device: bucket of every clipped offset j - p; NULL without a
+                             table.  An entry outside [0, n_buckets) is read as bucket 0 and reported to
+                             dev_status as CALIBATT_E_CORRUPT                                                   */
+  int32_t n_buckets, max_distance; /* at most 256 buckets, a distance of at most 2^20                           */
+  const uint8_t* mask;    /* [n_maps, ceil(Nq / 128), ceil(Nk / 128)] device, nonzero = kept, or NULL; head h
+                             uses map map_offset + h, the batch shares it                                       */
+  int32_t n_maps, map_offset;
+} calibatt_score;
+
+/*
+ * calibatt_attn_spans -- the interval of keys [lo, hi) every query row sees.
+ * Row i of batch entry b stands at position p = q_start[b] + i (q_start NULL:
+ * 0).  Without documents its keys are [0, kv_len[b]); with documents (packed
+ * back to back) those of the document that holds p, cut at kv_len[b]; with
+ * `causal`, of these only j <= p and the first prefix[b, m] keys of document m
+ * (a prefix is seen by every row of its document, its own rows included).
+ * Rows i >= q_len[b] and positions outside every document see nothing.
+ *  docs    [B, n_docs + 1] int32 device, ascending bounds (repeated bounds:
+ *          an empty document), or NULL with n_docs = 0;
+ *  prefix  [B, max(n_docs, 1)] int32 device or NULL (needs `causal`);
+ *  kv_len, q_len, q_start  [B] int32 device or NULL (Nk, Nq, 0); lengths are
+ *          clamped to [0, Nk] and [0, Nq], positions to +-2^30;
+ *  row_out, tile_out, q_start_out  the three arrays of calibatt_spans.
+ * One small kernel, made once per batch layout and used by every layer's
+ * calls.  Asynchronous.  Nq, Nk up to 2^24.
+ * Errors: CALIBATT_E_INVALID for sizes, a NULL or unaligned output, docs
+ * without n_docs, a prefix without `causal`.
+ */
+int calibatt_attn_spans(int B, int Nq, int Nk, int causal, const int32_t* docs, int n_docs, const int32_t* prefix,
+                        const int32_t* kv_len, const int32_t* q_len, const int32_t* q_start, int32_t* row_out,
+                        int32_t* tile_out, int32_t* q_start_out, calibatt_stream_t stream);
+
+/*
+ * calibatt_relative_buckets -- the usual bucket map of a learned relative
+ * position bias: with m = n_buckets (half of it when bidirectional) and e =
+ * m / 2, a distance below e has its own bucket, a distance x >= e bucket
+ * min(m - 1, e + floor((m - e) ln(x / e) / ln(max_distance / e))); when
+ * bidirectional, keys after the query use the upper half of the buckets, else
+ * they all fall into bucket 0.  Host arithmetic only.
+ *  out  host int32 [2 max_distance + 1] (written): offset -max_distance ...
+ *       max_distance.
+ * Errors: CALIBATT_E_INVALID for a NULL output, an odd bidirectional
+ * n_buckets, e < 1 or max_distance <= e; CALIBATT_E_UNSUPPORTED above 256
+ * buckets or a distance of 2^20.
+ */
+int calibatt_relative_buckets(int n_buckets, int max_distance, int bidirectional, int32_t* out);
+
+/*
+ * calibatt_score_attn_fwd -- O and LSE of the definition above.
+ *  q, o  [B, H, Nq, d];  k, v  [B, Hkv, Nk, d] of `dtype`;  lse [B, H, Nq]
+ *  float32 or NULL.  H a multiple of Hkv; d in {64, 128}; CALIBATT_BF16
+ *  (tcgen05 tensor cores, fp32 accumulation, probabilities rounded to bf16
+ *  for the second product) or CALIBATT_FP32 (FFMA).
+ *  workspace  device, 256-byte aligned, of at least
+ *             calibatt_score_attn_fwd_workspace_size bytes (0: may be NULL).
+ * Few query rows against many keys are split along the keys and joined by a
+ * second kernel in a fixed order.  Deterministic; asynchronous.
+ * Errors: CALIBATT_E_INVALID for NULL or unaligned pointers, sizes, strides,
+ * a scale or cap out of range, spans of other sizes, maps beyond n_maps;
+ * CALIBATT_E_UNSUPPORTED for another d or type, B or H above 65 535, lengths
+ * above 2^24 or B H N at 2^31 rows; CALIBATT_E_WORKSPACE; CALIBATT_E_CUDA.
+ */
+int calibatt_score_attn_fwd_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int dtype, size_t* bytes);
+int calibatt_score_attn_fwd(const calibatt_tensor4* q, const calibatt_tensor4* k, const calibatt_tensor4* v,
+                            const calibatt_tensor4* o, float* lse, int B, int H, int Hkv, int Nq, int Nk, int d,
+                            int dtype, const calibatt_spans* spans, const calibatt_score* score, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status, calibatt_stream_t stream);
+
+/*
+ * calibatt_score_attn_bwd -- the gradients of the definition above, given dO
+ * and the forward's O and LSE (same spans and score).
+ *  dout, q, o, dq  [B, H, Nq, d];  k, v, dk, dv  [B, Hkv, Nk, d];  lse [B, H,
+ *  Nq] float32 (read);  dtable [H, n_buckets] of `dtype` (written) or NULL
+ *  (needs score->table).  The slopes have no gradient.
+ *  workspace  device, 256-byte aligned, of at least
+ *             calibatt_score_attn_bwd_workspace_size bytes (n_buckets: 0
+ *             without dtable).
+ * Every gradient is summed in a fixed order without atomics: deterministic.
+ * The sums are float32 (the table's partial sums are joined in float64);
+ * CALIBATT_BF16 rounds P and dS to bf16 for their products.  Asynchronous.
+ * Errors: as calibatt_score_attn_fwd.
+ */
+int calibatt_score_attn_bwd_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int dtype, int n_buckets,
+                                           size_t* bytes);
+int calibatt_score_attn_bwd(const calibatt_tensor4* dout, const calibatt_tensor4* q, const calibatt_tensor4* k,
+                            const calibatt_tensor4* v, const calibatt_tensor4* o, const float* lse,
+                            const calibatt_tensor4* dq, const calibatt_tensor4* dk, const calibatt_tensor4* dv,
+                            void* dtable, int B, int H, int Hkv, int Nq, int Nk, int d, int dtype,
+                            const calibatt_spans* spans, const calibatt_score* score, void* workspace,
+                            size_t workspace_bytes, int32_t* dev_status, calibatt_stream_t stream);
+
+/*
  * calibatt_selftest_wait_timeout -- launches one block that waits, with the
  * bounded wait every kernel here uses, on a barrier that nothing completes.
  * After `limit_ns` it gives up and writes CALIBATT_E_TIMEOUT to dev_status.
