@@ -95,6 +95,51 @@ int make_tmap_bf16(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t co
   return CALIBATT_OK;
 }
 
+int make_tmap4_bf16(CUtensorMap* tm, const Tensor4& t, int B, int heads, int N, int d, int box_n, int box_h) {
+  std::call_once(g_encode_once, load_encode);
+  if (g_encode == nullptr) return set_error(CALIBATT_E_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(heads),
+                              static_cast<cuuint64_t>(B)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(t.sn) * 2, static_cast<cuuint64_t>(t.sh) * 2,
+                                 static_cast<cuuint64_t>(t.sb) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_n), static_cast<cuuint32_t>(box_h), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t.p, dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(CALIBATT_E_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+  return CALIBATT_OK;
+}
+
+int configure_kernel(const void* kern, std::atomic<bool>* done, size_t smem, int regs, const char* what) {
+  int dev = 0;
+  if (int rc = current_device(&dev)) return rc;
+  if (done[dev].load(std::memory_order_acquire)) return CALIBATT_OK;   // the set-up is idempotent: no lock
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return check_launch(what);
+  cudaFuncAttributes fa{};
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return check_launch(what);
+  if (fa.numRegs != regs)
+    return set_error(CALIBATT_E_UNSUPPORTED, "%s was built with %d registers per thread, expected %d", what, fa.numRegs,
+                     regs);
+  done[dev].store(true, std::memory_order_release);
+  return CALIBATT_OK;
+}
+
+int device_sms(int* sms) {
+  static std::atomic<int> known[kMaxDevices];
+  int dev = 0;
+  if (int rc = current_device(&dev)) return rc;
+  int n = known[dev].load(std::memory_order_acquire);
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return check_launch("cudaDeviceGetAttribute(SM count)");
+    known[dev].store(n, std::memory_order_release);
+  }
+  *sms = n;
+  return CALIBATT_OK;
+}
+
 // ---- self-test kernel: a wait that can only run out -------------------------
 
 namespace {

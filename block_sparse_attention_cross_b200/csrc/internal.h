@@ -1,6 +1,7 @@
 // internal.h -- host-side declarations shared by the calibatt translation units.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -110,6 +111,10 @@ struct ScoreArgs {
 // score_simt.cu (fp32, FFMA)
 int launch_score_fwd_simt(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
 int launch_score_bwd_simt(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
+// score_fwd.cu (bf16, tcgen05)
+bool score_packs(int G, int Nq, bool mask, bool table);
+int score_splits(int B, int heads, int nq_tiles, int nkb);
+int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s);
 // score_plan.cu
 int launch_attn_spans(int B, int Nq, int Nk, int causal, const int32_t* docs, int n_docs, const int32_t* prefix,
                       const int32_t* kv_len, const int32_t* q_len, const int32_t* q_start, int2* row, int4* tile,
@@ -134,5 +139,13 @@ int launch_selftest_timeout(uint64_t limit_ns, int32_t* status, cudaStream_t s);
 
 // TMA descriptor for a row-major bf16 matrix [rows, cols]; box 64 cols x box_rows rows, 128-byte swizzle.
 int make_tmap_bf16(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows = 128);
+
+// TMA descriptor of a bf16 [B, heads, N, d] tensor; box 64 cols x box_n rows x box_h heads, 128-byte swizzle.
+// Rows past N read as zero.
+int make_tmap4_bf16(CUtensorMap* tm, const Tensor4& t, int B, int heads, int N, int d, int box_n, int box_h);
+// Dynamic shared-memory limit of a kernel, set once per device (done[kMaxDevices]), and its launch register count (the register
+// re-split inside the kernel is sized for exactly `regs`).
+int configure_kernel(const void* kern, std::atomic<bool>* done, size_t smem, int regs, const char* what);
+int device_sms(int* sms);
 
 }  // namespace calibatt

@@ -111,6 +111,22 @@ int check_score(ScoreArgs& a, int B, int H, int Hkv, int Nq, int Nk, int d, int 
   return CALIBATT_OK;
 }
 
+// Forward workspace: [part_o][part_lse] of `splits` key splits.
+size_t fwd_layout(ScoreArgs& a, int d, void* ws) {
+  if (a.splits <= 1) return 0;
+  char* p = static_cast<char*>(ws);
+  const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq * a.splits;
+  a.part_o = reinterpret_cast<float*>(p);
+  const size_t off = align256(rows * d * 4);
+  a.part_lse = reinterpret_cast<float*>(p + off);
+  return off + align256(rows * 4);
+}
+
+void fwd_plan(ScoreArgs& a, bool packed) {
+  a.packed = packed;
+  a.splits = score_splits(a.B, packed ? a.Hkv : a.H, packed ? 1 : a.nqb, a.nkb);
+}
+
 // Backward workspace: [row_lse][row_d][part_table], 256-byte aligned pieces.
 size_t bwd_layout(ScoreArgs& a, int dtype, void* ws) {
   (void)dtype;
@@ -180,6 +196,15 @@ int calibatt_score_attn_fwd_workspace_size(int B, int H, int Hkv, int Nq, int Nk
   if (bytes == nullptr) return set_error(CALIBATT_E_INVALID, "bytes is NULL");
   if (int rc = check_sizes(B, H, Hkv, Nq, Nk, d, dtype)) return rc;
   *bytes = 0;
+  if (dtype != CALIBATT_BF16) return CALIBATT_OK;
+  // enough for every score function and mask of these sizes
+  ScoreArgs a{};
+  a.B = B; a.H = H; a.Hkv = Hkv; a.G = H / Hkv; a.Nq = Nq; a.nqb = (Nq + 127) / 128; a.nkb = (Nk + 127) / 128;
+  for (int packed = 0; packed < 2; ++packed) {
+    if (packed && !score_packs(a.G, Nq, false, false)) continue;
+    fwd_plan(a, packed != 0);
+    *bytes = std::max(*bytes, fwd_layout(a, d, nullptr));
+  }
   return CALIBATT_OK;
 }
 
@@ -200,9 +225,14 @@ int calibatt_score_attn_fwd(const calibatt_tensor4* q, const calibatt_tensor4* k
   a.o = to_tensor(o, B, H, Nq, d);
   a.lse = lse;
   a.status = dev_status;
-  (void)workspace;
-  (void)workspace_bytes;
-  return launch_score_fwd_simt(a, d, dtype, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == CALIBATT_FP32) return launch_score_fwd_simt(a, d, dtype, s);
+  fwd_plan(a, score_packs(a.G, Nq, a.mask != nullptr, a.table != nullptr));
+  const size_t need = fwd_layout(a, d, workspace);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
+    return set_error(CALIBATT_E_WORKSPACE, "workspace of %zu bytes (256-byte aligned) needed, %zu given", need,
+                     workspace_bytes);
+  return launch_score_fwd_tc(a, d, s);
 }
 
 int calibatt_score_attn_bwd_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int dtype, int n_buckets,

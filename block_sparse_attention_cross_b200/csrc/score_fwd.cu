@@ -1,0 +1,795 @@
+// score_fwd.cu -- score-modified attention forward on the tensor cores (bf16).
+//
+// The pipeline is the block-sparse forward's: a persistent CTA per SM holds
+// two query tiles ("slots") of 128 rows, one thread per query row; the tensor
+// core alternates between the slots, so that one slot's softmax runs while the
+// other slot's products do.  Warps 0-3 and 4-7: softmax of slots 0 and 1;
+// warps 8 and 11: TMA producers, one K/V ring each; warp 9 issues every
+// tcgen05.mma; warp 10 idles.  TMEM: slot s owns columns [256 s, 256 s + 256):
+// scores at + 0 (the probabilities overwrite their first half as bf16 pairs,
+// the A operand of the second product), O at + 128.
+//
+// What differs:
+//  - a tile walks the 128-key tiles of its rows' interval range, restricted to
+//    the calibrated mask's kept blocks where one is given, and only tiles
+//    that the interval of some row cuts pay for an element mask;
+//  - the scores pass through the cap, the distance bias and the table before
+//    the softmax, in registers;
+//  - tensors are 4-D maps with their own strides, so lengths need no padding
+//    and rows past a length read as zero;
+//  - the G query heads of a key head share one tile when their rows fit (few
+//    queries: rows g Nq + i), so K and V are read once for all of them;
+//  - few tiles against many keys are split along the keys; k_score_join adds
+//    the splits' results in a fixed order.
+// Bound: MUFU and tensor core together for long queries (see the figures at
+// the launch), HBM for few queries.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "score_common.cuh"
+
+namespace calibatt {
+namespace {
+
+constexpr int TILE = 128;
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;
+constexpr uint32_t kSoftmaxRegs = 192;
+constexpr uint32_t kControlRegs = 120;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
+constexpr int kProducer0 = 8, kMma = 9, kProducer1 = 11;
+constexpr uint32_t kTmemCols = 512;
+// The reference maximum is raised, and O rescaled, only when a tile's maximum
+// exceeds it by more than this many log2 units: P stays below 2^64.
+constexpr float kRescaleThreshold = 64.0f;
+constexpr int kMaxPackedTable = 8;   // heads of a packed tile with a table (windows in shared memory)
+
+template <int D>
+struct Layout {
+  static constexpr uint32_t BOX = TILE * 64 * 2;         // 128 rows x 64 columns, one swizzle span
+  static constexpr uint32_t TBYTES = TILE * D * 2;       // one Q, K or V tile
+  static constexpr uint32_t WIN = kMaxPackedTable * 256 * 4;   // bias windows of one step
+  static constexpr int RING = D == 128 ? 2 : 4;          // K/V tiles per slot
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_RING = 2 * TBYTES;
+  static constexpr uint32_t OFF_WIN = OFF_RING + 2 * RING * TBYTES;   // [2 slots][WIN]
+  static constexpr uint32_t OFF_CTRL = OFF_WIN + 2 * WIN;
+  static constexpr uint32_t SMEM = OFF_CTRL + 1024 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+template <int RING>
+struct Ctrl {
+  uint64_t ring_full[2][RING], ring_empty[2][RING];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2];
+  uint64_t o_full[2], o_free[2];
+  uint64_t sync[2];     // the 128 softmax threads of a slot
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  uint32_t bad[2][4];   // keys of a slot's V tile that hold a non-finite value
+};
+
+template <int V>
+using IntC = std::integral_constant<int, V>;
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+__device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tma_load_4d_w(void* dst, const CUtensorMap* tm, int x, int n, int h, int b, uint64_t* bar,
+                                              uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(n), "r"(h), "r"(b), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+
+struct FwdArgs {
+  ScoreArgs a;
+  int Hx;       // heads of the tile grid: Hkv where the G heads share a tile, else H
+  int nq;       // query tiles per head of the grid
+  int hgroup;   // heads walked together, see tile_at
+  int T;        // tiles
+};
+
+// One tile of the walk and its current key tile.  Every role evaluates the
+// same data, warp-collectively, so all agree.
+struct Walk {
+  int b, hx, qb, sp;
+  int kb, next, hi;      // current and next kept key tile (-1: none), end of the range
+  uint32_t word;         // mask: kept tiles after `next` in the 32 tiles from wbase on
+  int wbase;
+};
+
+// Order of the tiles: heads in groups whose K and V fit well into L2, and
+// inside a group query tiles from the last to the first, all heads of one
+// query tile together: under a causal rule the longest walks come first, so
+// the static round-robin over slots stays balanced.  Splits innermost.
+__device__ __forceinline__ void tile_at(const FwdArgs& f, int t, Walk& w) {
+  w.sp = t % f.a.splits;
+  int u = t / f.a.splits;
+  const int BH = f.a.B * f.Hx;
+  const int g = u / (f.hgroup * f.nq);
+  const int base = g * f.hgroup, size = min(f.hgroup, BH - base);
+  u -= base * f.nq;
+  w.qb = f.nq - 1 - u / size;
+  const int bh = base + u % size;
+  w.b = bh / f.Hx;
+  w.hx = bh % f.Hx;
+}
+
+__device__ __forceinline__ int walk_find(const FwdArgs& f, Walk& w) {
+  while (w.word == 0) {
+    w.wbase += 32;
+    if (w.wbase >= w.hi) return -1;
+    const int kb = w.wbase + lane_id();
+    w.word = __ballot_sync(0xffffffffu, kb < w.hi && score_kept(f.a, w.hx, w.qb, kb));
+  }
+  const int kb = w.wbase + __ffs(w.word) - 1;
+  w.word &= w.word - 1;
+  return kb;
+}
+
+__device__ __forceinline__ int walk_after(const FwdArgs& f, Walk& w, int kb) {
+  if (f.a.mask != nullptr) return walk_find(f, w);
+  return kb + 1 < w.hi ? kb + 1 : -1;
+}
+
+// Starts tile t; returns whether it has a key tile.
+__device__ __forceinline__ bool walk_start(const FwdArgs& f, int t, Walk& w) {
+  tile_at(f, t, w);
+  const int4 r = score_tile(f.a, w.b, w.qb);
+  int lo = r.x >> 7;
+  w.hi = (r.y + TILE - 1) >> 7;
+  if (f.a.splits > 1 && w.hi > lo) {
+    const int per = (w.hi - lo + f.a.splits - 1) / f.a.splits;
+    lo = min(w.hi, lo + w.sp * per);
+    w.hi = min(w.hi, lo + per);
+  }
+  if (r.x >= r.y) w.hi = lo;
+  w.word = 0;
+  if (f.a.mask != nullptr) {
+    w.wbase = lo - 32;
+    w.kb = walk_find(f, w);
+  } else {
+    w.kb = lo < w.hi ? lo : -1;
+  }
+  w.next = w.kb < 0 ? -1 : walk_after(f, w, w.kb);
+  return w.kb >= 0;
+}
+
+// The producer's and the MMA warp's position: key tiles of this slot's
+// non-empty tiles, one after the other.
+struct Cursor {
+  Walk w;
+  int t;
+  bool first, done;
+};
+
+__device__ __forceinline__ void cursor_seek(const FwdArgs& f, Cursor& c, int stride) {
+  while (c.t < f.T) {
+    if (walk_start(f, c.t, c.w)) {
+      c.first = true;
+      return;
+    }
+    c.t += stride;
+  }
+  c.done = true;
+}
+
+__device__ __forceinline__ void cursor_next(const FwdArgs& f, Cursor& c, int stride) {
+  if (c.w.next >= 0) {
+    c.first = false;
+    c.w.kb = c.w.next;
+    c.w.next = walk_after(f, c.w, c.w.kb);
+  } else {
+    c.t += stride;
+    cursor_seek(f, c, stride);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_score_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdArgs f) {
+  using L = Layout<D>;
+  constexpr int R = L::RING;
+  const ScoreArgs& a = f.a;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Ctrl<R>* c = reinterpret_cast<Ctrl<R>*>(smem + L::OFF_CTRL);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int stride = 2 * gridDim.x;
+
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      for (int e = 0; e < R; ++e) {
+        mbar_init(&c->ring_full[s][e], 1);
+        mbar_init(&c->ring_empty[s][e], 1);
+      }
+      mbar_init(&c->q_full[s], 1);
+      mbar_init(&c->q_empty[s], 1);
+      mbar_init(&c->s_full[s], 1);
+      mbar_init(&c->p_full[s], 128);
+      mbar_init(&c->o_full[s], 1);
+      mbar_init(&c->o_free[s], 128);
+      mbar_init(&c->sync[s], 128);
+    }
+    mbar_init(&c->drain, 1);
+    c->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == kMma) {
+    tmem_alloc(&c->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem_base;
+
+  if (warp >= 8) regs_dec<kControlRegs>();
+  if (warp == kProducer0 || warp == kProducer1) {
+    // ===================== TMA producer of one slot ===========================
+    const int s = warp == kProducer1;
+    Cursor cu;
+    cu.t = blockIdx.x + s * gridDim.x;
+    cu.done = false;
+    cursor_seek(f, cu, stride);
+    uint32_t g = 0;
+    int qf = 0;
+    bool ok = true;
+    const uint64_t pol = l2_policy_evict_last(), pol_q = l2_policy_evict_first();
+    uint8_t* ring = smem + L::OFF_RING + s * R * L::TBYTES;
+    const uint32_t q_bytes = a.packed ? static_cast<uint32_t>(a.G * a.Nq * D * 2) : L::TBYTES;
+    while (ok && !cu.done) {
+      const Walk& w = cu.w;
+      if (cu.first) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&c->q_empty[s], (qf & 1) ^ 1, &c->abort, a.spin_ns));
+        if (!ok) break;
+        mbar_arrive_expect_tx_w(&c->q_full[s], q_bytes);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+          tma_load_4d_w(smem + L::OFF_Q + s * L::TBYTES + x * L::BOX, &tmQ, x * 64, w.qb * TILE,
+                        a.packed ? w.hx * a.G : w.hx, w.b, &c->q_full[s], pol_q);
+        ++qf;
+      }
+      const int hk = a.packed ? w.hx : w.hx / a.G;
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const int e = g % R;
+        ok = __all_sync(0xffffffffu, mbar_wait(&c->ring_empty[s][e], ((g / R) & 1) ^ 1, &c->abort, a.spin_ns));
+        if (!ok) break;
+        mbar_arrive_expect_tx_w(&c->ring_full[s][e], L::TBYTES);
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+          tma_load_4d_w(ring + e * L::TBYTES + x * L::BOX, kv ? &tmV : &tmK, x * 64, w.kb * TILE, hk, w.b,
+                        &c->ring_full[s][e], pol);
+        ++g;
+      }
+      cursor_next(f, cu, stride);
+    }
+    if (lane == 0) {
+      if (!ok) {
+        c->abort = 1;
+        report_status(a.status, CALIBATT_E_TIMEOUT);
+      }
+      // Drain: every copy issued must have landed before the CTA may exit.
+      for (int e = 0; e < R; ++e) {
+        const uint32_t fills = (g > static_cast<uint32_t>(e)) ? (g - 1 - e) / R + 1 : 0;
+        if (fills > 0) mbar_wait(&c->ring_full[s][e], (fills - 1) & 1, nullptr, a.spin_ns);
+      }
+      if (qf > 0) mbar_wait(&c->q_full[s], (qf - 1) & 1, nullptr, a.spin_ns);
+    }
+  } else if (warp == kMma) {
+    // ===================== MMA issuer =========================================
+    // Per key tile of a slot: S, then (once the probabilities are stored) the
+    // second product and the slot's next S; the slots are served in turn.
+    Cursor cu0, cu1;
+    cu0.t = blockIdx.x;
+    cu1.t = blockIdx.x + gridDim.x;
+    cu0.done = cu1.done = false;
+    cursor_seek(f, cu0, stride);
+    cursor_seek(f, cu1, stride);
+    constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, TILE, false);
+    constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D, true);
+    uint32_t g0 = 0, g1 = 0, gb0 = 0, gb1 = 0;
+    int qt0 = 0, qt1 = 0, ot0 = 0, ot1 = 0;
+    bool ok = true;
+    auto issue_s = [&](auto s_c) {
+      constexpr int s = decltype(s_c)::value;
+      Cursor& cu = s ? cu1 : cu0;
+      uint32_t& g = s ? g1 : g0;
+      int& qt = s ? qt1 : qt0;
+      const int e = g % R;
+      const bool w = (!cu.first || mbar_wait(&c->q_full[s], qt & 1, &c->abort, a.spin_ns)) &&
+                     mbar_wait(&c->ring_full[s][e], (g / R) & 1, &c->abort, a.spin_ns);
+      if (!__all_sync(0xffffffffu, w)) return false;
+      tc_fence_after();
+      const uint32_t sQ = smem_u32(smem + L::OFF_Q + s * L::TBYTES);
+      const uint32_t sK = smem_u32(smem + L::OFF_RING + (s * R + e) * L::TBYTES);
+      const uint32_t tS = tmem + s * 256;
+      if (D == 128) {
+        mma_ss_k128_w(tS, sdesc_sw128(sQ, 16, 1024), sdesc_sw128(sK, 16, 1024), IDESC_S, L::BOX >> 4);
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_bf16_ss_w(tS, sdesc_sw128(sQ + kk * 32, 16, 1024), sdesc_sw128(sK + kk * 32, 16, 1024), IDESC_S,
+                        kk > 0 ? 1u : 0u);
+      }
+      mma_commit_w(&c->s_full[s]);
+      mma_commit_w(&c->ring_empty[s][e]);
+      if (cu.first) ++qt;
+      if (cu.w.next < 0) mma_commit_w(&c->q_empty[s]);
+      ++g;
+      return true;
+    };
+    auto issue_pv = [&](auto s_c) {
+      constexpr int s = decltype(s_c)::value;
+      Cursor& cu = s ? cu1 : cu0;
+      uint32_t& g = s ? g1 : g0;
+      uint32_t& gb = s ? gb1 : gb0;
+      int& ot = s ? ot1 : ot0;
+      const int e = g % R;
+      const uint32_t tS = tmem + s * 256;
+      const uint64_t vd = sdesc_sw128(smem_u32(smem + L::OFF_RING + (s * R + e) * L::TBYTES), L::BOX, 1024);
+      mma_ts_k128_w(tS + 128, tS, vd, IDESC_O, cu.first ? 0u : 1u);
+      mma_commit_w(&c->ring_empty[s][e]);
+      if (cu.first) ++ot;
+      if (cu.w.next < 0) mma_commit_w(&c->o_full[s]);
+      ++g;
+      ++gb;
+      cursor_next(f, cu, stride);
+      return cu.done ? true : issue_s(s_c);
+    };
+    bool due0 = false, due1 = false;
+    if (!cu0.done) ok = due0 = issue_s(IntC<0>{});
+    if (ok && !cu1.done) ok = due1 = issue_s(IntC<1>{});
+    int turn = 0;
+    while (ok && (due0 || due1)) {
+      const int s = (due0 && (turn == 0 || !due1)) ? 0 : 1;
+      const Cursor& cu = s ? cu1 : cu0;
+      const uint32_t g = s ? g1 : g0;
+      const bool w = mbar_wait(&c->ring_full[s][g % R], (g / R) & 1, &c->abort, a.spin_ns) &&
+                     (!cu.first || mbar_wait(&c->o_free[s], ((s ? ot1 : ot0) & 1) ^ 1, &c->abort, a.spin_ns)) &&
+                     mbar_wait(&c->p_full[s], (s ? gb1 : gb0) & 1, &c->abort, a.spin_ns);
+      if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+      tc_fence_after();
+      if (s == 0) {
+        ok = issue_pv(IntC<0>{});
+        due0 = !cu0.done;
+      } else {
+        ok = issue_pv(IntC<1>{});
+        due1 = !cu1.done;
+      }
+      turn = s ^ 1;
+    }
+    if (!ok && lane == 0) {
+      c->abort = 1;
+      report_status(a.status, CALIBATT_E_TIMEOUT);
+    }
+    __syncwarp();
+    mma_commit_w(&c->drain);
+    mbar_wait(&c->drain, 0, nullptr, a.spin_ns);
+  } else if (warp < 8) {
+    // ===================== softmax warpgroups =================================
+    regs_inc<kSoftmaxRegs>();
+    const int slot = warp >> 2, w4 = warp & 3;
+    const int row = w4 * 32 + lane;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + slot * 256;
+    const uint32_t t_o = t_s + 128;
+    float* win = reinterpret_cast<float*>(smem + L::OFF_WIN + slot * L::WIN);
+    // Scores in log2 units.  Without a cap or bias the scale is folded into
+    // the exponential's FFMA; otherwise the transforms apply it.
+    const bool xform = a.cap > 0.f || a.slopes != nullptr || a.table != nullptr;
+    const float c2 = xform ? 1.f : a.scale * kLog2e;
+    const float capA = a.cap * kLog2e;
+    const float kcap = a.cap > 0.f ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+    const uint64_t c2x2 = f2pack(c2, c2);
+    uint32_t gb = 0;
+    int tiles = 0;
+    bool ok = true, corrupt = false;
+    // Barrier among the slot's softmax threads, bounded like every wait here
+    // (a bar.sync would hang if another warp of the slot gave up).
+    uint32_t sync_phase = 0;
+    auto slot_sync = [&]() {
+      mbar_arrive(&c->sync[slot]);
+      const bool w = mbar_wait(&c->sync[slot], sync_phase, &c->abort, a.spin_ns);
+      sync_phase ^= 1;
+      return static_cast<bool>(__all_sync(0xffffffffu, w));
+    };
+    for (int t = blockIdx.x + slot * gridDim.x; ok && t < f.T; t += stride) {
+      Walk w;
+      const bool any = walk_start(f, t, w);
+      // this thread's row
+      int h, i;
+      bool live;
+      if (a.packed) {
+        const int g = row / a.Nq;
+        i = row - g * a.Nq;
+        live = g < a.G;
+        h = w.hx * a.G + min(g, a.G - 1);
+      } else {
+        i = w.qb * TILE + row;
+        live = i < a.Nq;
+        h = w.hx;
+      }
+      const size_t orow = (static_cast<size_t>(w.b) * a.H + h) * a.Nq + i;   // of lse and the partial results
+      __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(a.o.p) + w.b * a.o.sb + h * a.o.sh + i * a.o.sn;
+      if (!any) {
+        if (live) {
+          if (a.splits > 1) {
+            a.part_lse[orow * a.splits + w.sp] = -INFINITY;
+          } else {
+            const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < D / 8; ++x) reinterpret_cast<uint4*>(op)[x] = z;
+            if (a.lse != nullptr) a.lse[orow] = -INFINITY;
+          }
+        }
+        continue;
+      }
+      const int4 tr = score_tile(a, w.b, w.qb);
+      const int2 vis = live ? score_row(a, w.b, i) : make_int2(0, 0);
+      const int p0 = a.q_start[w.b] + (a.packed ? 0 : w.qb * TILE);   // positions of the tile's rows: p0 ... p1
+      const int p1 = p0 + (a.packed ? a.Nq : TILE) - 1;
+      const int p = a.q_start[w.b] + i;
+      const float slope = a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
+      const __nv_bfloat16* tab =
+          reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
+      float far_lo = 0.f, far_hi = 0.f;
+      if (a.table != nullptr) {
+        far_lo = __bfloat162float(tab[score_bucket(a, -a.R, &corrupt)]) * kLog2e;
+        far_hi = __bfloat162float(tab[score_bucket(a, a.R, &corrupt)]) * kLog2e;
+      }
+      float m = -INFINITY, l = 0.f, s_best = -INFINITY;
+      bool row_bad = false;
+      for (bool first = true;; first = false, ++gb) {
+        const int k0 = w.kb * TILE;
+        const bool edge = k0 < tr.z || k0 + TILE > tr.w;
+        const bool near = a.table != nullptr && k0 - p1 < a.R && k0 + TILE - 1 - p0 > -a.R;
+        if (near) {
+          // The table's values of the offsets k0 - p1 ... k0 + 127 - p0 of
+          // this tile, per head: 255 values, read with the row's own shift.
+          if (!(ok = slot_sync())) break;   // the previous window is read
+          const int heads = a.packed ? a.G : 1, h0 = a.packed ? w.hx * a.G : w.hx;
+          const int len = TILE + p1 - p0;
+          for (int x = row; x < len; x += TILE) {
+            const int n = score_bucket(a, k0 - p1 + x, &corrupt);
+            for (int g = 0; g < heads; ++g)
+              win[g * 256 + x] = kLog2e * __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(
+                                              a.table)[static_cast<size_t>(h0 + g) * a.n_buckets + n]);
+          }
+          if (!(ok = slot_sync())) break;
+        }
+        const bool got = mbar_wait(&c->s_full[slot], gb & 1, &c->abort, a.spin_ns);
+        ok = __all_sync(0xffffffffu, got);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[TILE];
+#pragma unroll
+        for (int q4 = 0; q4 < TILE / 32; ++q4)
+          tmem_ld32(t_s + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[q4 * 32]));
+        tmem_ld_wait();
+        reg_fence(r);
+        // cap tanh(x) = cap - 2 cap / (1 + e^(2x)): exact at both ends, and
+        // the MUFU's relative errors stay 1e-7 of the cap
+        if (a.cap > 0.f) {
+#pragma unroll
+          for (int x = 0; x < TILE; ++x)
+            r[x] = f2u(fmaf(-2.f * capA, rcp_approx(1.f + ex2_approx(u2f(r[x]) * kcap)), capA));
+        } else if (xform) {
+          const float sc = a.scale * kLog2e;
+#pragma unroll
+          for (int x = 0; x < TILE; ++x) r[x] = f2u(u2f(r[x]) * sc);
+        }
+        if (a.slopes != nullptr) {
+          const float d0 = static_cast<float>(k0 - p);
+#pragma unroll
+          for (int x = 0; x < TILE; ++x) r[x] = f2u(fmaf(-slope, fabsf(d0 + x), u2f(r[x])));
+        }
+        if (near) {
+          const float* wr = win + (a.packed ? min(row / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
+#pragma unroll
+          for (int x = 0; x < TILE; ++x) r[x] = f2u(u2f(r[x]) + wr[x]);
+        } else if (a.table != nullptr) {
+          const float far = k0 > p1 ? far_hi : far_lo;
+#pragma unroll
+          for (int x = 0; x < TILE; ++x) r[x] = f2u(u2f(r[x]) + far);
+        }
+        if (edge) {
+          // keys outside the row's interval
+          const int e0 = vis.x - k0, e1 = vis.y - k0;
+#pragma unroll
+          for (int x = 0; x < TILE; ++x)
+            if (x < e0 || x >= e1) r[x] = f2u(-INFINITY);
+          // A probability of 0 does not silence a NaN or infinity in V: rows of
+          // the V tile that hold one are zeroed before the second product, and
+          // the query rows that see such a key become NaN.
+          const uint32_t ge = 2 * gb + 1;
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&c->ring_full[slot][ge % R], (ge / R) & 1, &c->abort, a.spin_ns));
+          if (!ok) break;
+          uint8_t* vrow = smem + L::OFF_RING + (slot * R + ge % R) * L::TBYTES + row * 128;
+          uint32_t nonfinite = 0;
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch) {
+              const uint4 u = *reinterpret_cast<const uint4*>(vrow + x * L::BOX + ((ch ^ (row & 7)) << 4));
+              // an exponent of all ones carries into the sign's place
+              nonfinite |= ((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+                           ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u);
+            }
+          const bool bad = (nonfinite & 0x80008000u) != 0;
+          const uint32_t bw = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) c->bad[slot][w4] = bw;
+          if (bad) {
+            const uint4 z = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+              for (int ch = 0; ch < 8; ++ch) *reinterpret_cast<uint4*>(vrow + x * L::BOX + (ch << 4)) = z;
+          }
+          fence_proxy_async_smem();
+          if (!(ok = slot_sync())) break;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            // keys 32 q ... 32 q + 31 of the tile that this row sees
+            const int s0 = min(max(e0 - 32 * q, 0), 32), s1 = min(max(e1 - 32 * q, 0), 32);
+            const uint32_t below1 = s1 >= 32 ? 0xffffffffu : (1u << s1) - 1u;
+            const uint32_t below0 = s0 >= 32 ? 0xffffffffu : (1u << s0) - 1u;
+            row_bad |= (c->bad[slot][q] & below1 & ~below0) != 0;
+          }
+          if (!(ok = slot_sync())) break;
+        }
+        float mx0 = u2f(r[0]), mx1 = u2f(r[1]), mx2 = u2f(r[2]), mx3 = u2f(r[3]);
+#pragma unroll
+        for (int x = 4; x + 8 <= TILE; x += 8) {
+          mx0 = fmax3(mx0, u2f(r[x + 0]), u2f(r[x + 1]));
+          mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
+          mx2 = fmax3(mx2, u2f(r[x + 4]), u2f(r[x + 5]));
+          mx3 = fmax3(mx3, u2f(r[x + 6]), u2f(r[x + 7]));
+        }
+        mx0 = fmax3(mx0, u2f(r[TILE - 4]), u2f(r[TILE - 3]));
+        mx1 = fmax3(mx1, u2f(r[TILE - 2]), u2f(r[TILE - 1]));
+        const float bmax = fmax3(mx0, mx1, fmaxf(mx2, mx3));
+        s_best = fmaxf(s_best, bmax);
+        // The reference: the first tile's maximum, raised (and O and l
+        // rescaled) only by more than the threshold.  While a row has seen
+        // nothing it is -inf and the exponent's shift 0.
+        float alpha = 1.f;
+        bool rescale = false;
+        const float m_cand = bmax * c2;
+        if (first) {
+          m = m_cand;
+        } else {
+          const bool raise = m_cand > m + kRescaleThreshold;
+          rescale = __any_sync(0xffffffffu, raise);
+          if (raise) {
+            alpha = ex2_approx(m - m_cand);
+            m = m_cand;
+          }
+        }
+        const float neg = m == -INFINITY ? 0.f : -m;
+        const uint64_t negm = f2pack(neg, neg);
+        uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+#pragma unroll
+        for (int c16 = 0; c16 < TILE / 32; ++c16) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int e = c16 * 32 + 2 * x;
+            const uint64_t y = ffma2(f2pack(u2f(r[e]), u2f(r[e + 1])), c2x2, negm);
+            float xl, xh;
+            f2unpack(y, xl, xh);
+            const uint64_t pv = f2pack(ex2_approx(xl), ex2_approx(xh));
+            if (x & 1) acc1 = fadd2(acc1, pv); else acc0 = fadd2(acc0, pv);
+            float pl, ph;
+            f2unpack(pv, pl, ph);
+            pk[x] = pack_bf16x2(pl, ph);
+          }
+          tmem_st16(t_s + c16 * 16, pk);
+        }
+        if (rescale) {
+#pragma unroll
+          for (int q4 = 0; q4 < D / 32; ++q4) {
+            uint32_t ro[32];
+            tmem_ld32(t_o + q4 * 32, ro);
+            tmem_ld_wait();
+            reg_fence(ro);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) ro[x] = f2u(u2f(ro[x]) * alpha);
+            tmem_st32(t_o + q4 * 32, ro);
+          }
+        }
+        float a0, a1, b0, b1;
+        f2unpack(acc0, a0, a1);
+        f2unpack(acc1, b0, b1);
+        l = l * alpha + ((a0 + a1) + (b0 + b1));
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&c->p_full[slot]);
+        if (w.next < 0) { ++gb; break; }
+        w.kb = w.next;
+        w.next = walk_after(f, w, w.kb);
+      }
+      if (!ok) break;
+      // ---- epilogue: O / l, LSE.  As in the block-sparse forward, the
+      // rounding error of the row's largest probability moves into the
+      // normaliser, so that a row with one dominant key returns its value.
+      const float p_best = ex2_approx(fmaf(s_best, c2, -m));
+      const float corr = __uint_as_float(pack_bf16x2(p_best, 0.f) << 16) - p_best;
+      ok = __all_sync(0xffffffffu, mbar_wait(&c->o_full[slot], tiles & 1, &c->abort, a.spin_ns));
+      if (!ok) break;
+      ++tiles;
+      tc_fence_after();
+      const float inv_l = row_bad ? NAN : l == 0.f ? 0.f : 1.f / (l + corr);
+      const float row_lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      if (a.splits > 1) {
+        float* po = a.part_o + (orow * a.splits + w.sp) * D;
+#pragma unroll
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t ro[32];
+          tmem_ld32(t_o + q4 * 32, ro);
+          tmem_ld_wait();
+          reg_fence(ro);
+          if (live) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              reinterpret_cast<float4*>(po + q4 * 32)[x] =
+                  make_float4(u2f(ro[4 * x]) * inv_l, u2f(ro[4 * x + 1]) * inv_l, u2f(ro[4 * x + 2]) * inv_l,
+                              u2f(ro[4 * x + 3]) * inv_l);
+          }
+        }
+        if (live) a.part_lse[orow * a.splits + w.sp] = row_lse;
+      } else {
+#pragma unroll
+        for (int q4 = 0; q4 < D / 32; ++q4) {
+          uint32_t ro[32];
+          tmem_ld32(t_o + q4 * 32, ro);
+          tmem_ld_wait();
+          reg_fence(ro);
+          if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(op + q4 * 32);
+#pragma unroll
+            for (int v4 = 0; v4 < 4; ++v4)
+              dst[v4] = make_uint4(pack_bf16x2(u2f(ro[8 * v4 + 0]) * inv_l, u2f(ro[8 * v4 + 1]) * inv_l),
+                                   pack_bf16x2(u2f(ro[8 * v4 + 2]) * inv_l, u2f(ro[8 * v4 + 3]) * inv_l),
+                                   pack_bf16x2(u2f(ro[8 * v4 + 4]) * inv_l, u2f(ro[8 * v4 + 5]) * inv_l),
+                                   pack_bf16x2(u2f(ro[8 * v4 + 6]) * inv_l, u2f(ro[8 * v4 + 7]) * inv_l));
+          }
+        }
+        if (live && a.lse != nullptr) a.lse[orow] = row_lse;
+      }
+      tc_fence_before();
+      mbar_arrive(&c->o_free[slot]);
+    }
+    if (!ok) {
+      c->abort = 1;
+      report_status(a.status, CALIBATT_E_TIMEOUT);
+    }
+    if (corrupt) report_status(a.status, CALIBATT_E_CORRUPT);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+// Joins the splits of a row: weights 2^(lse_s - max), in split order.  One
+// warp a row, a lane D / 32 columns; reads the partial results once.
+template <int D>
+__global__ void __launch_bounds__(128) k_score_join(const ScoreArgs a) {
+  const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
+  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const int lane = threadIdx.x & 31;
+  const float* pl = a.part_lse + r * a.splits;
+  float mx = -INFINITY;
+  bool nan = false;
+  for (int s = lane; s < a.splits; s += 32) {
+    mx = fmaxf(mx, pl[s]);
+    nan |= isnan(pl[s]);
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+  nan = __any_sync(0xffffffffu, nan);
+  float acc[D / 32] = {}, l = 0.f;
+  if (mx != -INFINITY) {
+    for (int s = 0; s < a.splits; ++s) {
+      const float x = pl[s];
+      if (x == -INFINITY) continue;   // its partial O was not written
+      const float wgt = expf(x - mx);
+      l += wgt;
+      const float* po = a.part_o + (r * a.splits + s) * D + lane * (D / 32);
+#pragma unroll
+      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(wgt, po[e], acc[e]);
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int i = static_cast<int>(r % a.Nq);
+  const int bh = static_cast<int>(r / a.Nq), b = bh / a.H, h = bh % a.H;
+  __nv_bfloat16* op =
+      reinterpret_cast<__nv_bfloat16*>(a.o.p) + b * a.o.sb + h * a.o.sh + i * a.o.sn + lane * (D / 32);
+#pragma unroll
+  for (int e = 0; e < D / 32; e += 2)
+    *reinterpret_cast<uint32_t*>(op + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && a.lse != nullptr) a.lse[r] = nan ? NAN : l == 0.f ? -INFINITY : mx + logf(l);
+}
+
+template <int D>
+int launch(const ScoreArgs& a, int sms, cudaStream_t s) {
+  FwdArgs f;
+  f.a = a;
+  f.Hx = a.packed ? a.Hkv : a.H;
+  f.nq = a.packed ? 1 : a.nqb;
+  // K and V of a group of heads: up to 64 MB of the 126 MB L2
+  const long long head_bytes = 4ll * a.Nk * D;
+  const long long per = a.packed ? 1 : a.G;   // grid heads of one key head
+  f.hgroup = static_cast<int>(std::min<long long>(std::max<long long>(1, (64ll << 20) / head_bytes) * per,
+                                                  static_cast<long long>(a.B) * f.Hx));
+  const long long T = static_cast<long long>(a.B) * f.Hx * f.nq * a.splits;
+  if (T >= (1ll << 31)) return set_error(CALIBATT_E_UNSUPPORTED, "too many query tiles");
+  f.T = static_cast<int>(T);
+  CUtensorMap tq, tk, tv;
+  int rc;
+  if ((rc = make_tmap4_bf16(&tq, a.q, a.B, a.H, a.Nq, D, a.packed ? a.Nq : TILE, a.packed ? a.G : 1))) return rc;
+  if ((rc = make_tmap4_bf16(&tk, a.k, a.B, a.Hkv, a.Nk, D, TILE, 1))) return rc;
+  if ((rc = make_tmap4_bf16(&tv, a.v, a.B, a.Hkv, a.Nk, D, TILE, 1))) return rc;
+  auto kern = k_score_fwd<D>;
+  static std::atomic<bool> done[kMaxDevices];
+  if ((rc = configure_kernel(reinterpret_cast<const void*>(kern), done, Layout<D>::SMEM, kLaunchRegs, "k_score_fwd")))
+    return rc;
+  const int grid = static_cast<int>(std::min<long long>(sms, T));
+  kern<<<grid, kThreads, Layout<D>::SMEM, s>>>(tq, tk, tv, f);
+  count_launch();
+  if ((rc = check_launch("k_score_fwd"))) return rc;
+  if (a.splits > 1) {
+    const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
+    k_score_join<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(a);
+    count_launch();
+    return check_launch("k_score_join");
+  }
+  return CALIBATT_OK;
+}
+
+}  // namespace
+
+// Whether the G query heads of a key head share a tile: their rows fit, no
+// mask (it may differ between the heads) and the table's windows fit.
+bool score_packs(int G, int Nq, bool mask, bool table) {
+  return G > 1 && static_cast<long long>(G) * Nq <= TILE && !mask && (!table || G <= kMaxPackedTable);
+}
+
+// Splits of the key axis.  296 slots (two on each of 148 SMs) want a tile
+// each; with fewer tiles than slots the keys are divided, but a split keeps
+// at least 4 key tiles.
+int score_splits(int B, int heads, int nq_tiles, int nkb) {
+  const long long tiles = static_cast<long long>(B) * heads * nq_tiles;
+  if (tiles >= 296) return 1;
+  const long long want = (296 + tiles - 1) / tiles;
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(want, nkb / 4)));
+}
+
+int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s) {
+  int sms = 0;
+  if (int rc = device_sms(&sms)) return rc;
+  return d == 128 ? launch<128>(a, sms, s) : launch<64>(a, sms, s);
+}
+
+}  // namespace calibatt
