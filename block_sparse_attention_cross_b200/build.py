@@ -21,7 +21,7 @@ BUILD = PKG / "_build"
 LIB = PKG / "libcalibatt.so"
 
 SOURCES = ["api.cu", "attn_tc.cu", "attn_fwd.cu", "attn_simt.cu", "select_vote.cu", "compile.cu", "noalloc.cu", "sharing.cu", "skiplist.cu", "gather.cu", "plan.cu", "similarity.cu",
-           "score_plan.cu", "score_rows.cu", "score_simt.cu", "score_fwd.cu", "score_api.cu"]
+           "score_plan.cu", "score_rows.cu", "score_simt.cu", "score_fwd.cu", "score_bwd.cu", "score_api.cu"]
 HEADERS = ["common.cuh", "internal.h", "score_common.cuh"]
 
 NVCC_FLAGS = [

@@ -100,8 +100,9 @@ struct ScoreArgs {
   int splits, packed;       // forward: splits of the key axis; packed: the G heads of a key head share a tile
   float* part_o;            // [B, H, Nq, splits, d]
   float* part_lse;          // [B, H, Nq, splits]
-  float* row_lse;           // backward: [B, H, 128 nqb] LSE, +inf where a row sees nothing
-  float* row_d;             // backward: [B, H, 128 nqb] sum over d of dO O
+  float* row_lse;           // backward: [B, H, 128 nqb], see score_rows.cu
+  float* row_d;             // backward: [B, H, 128 nqb]
+  int2* row_span;           // backward, bf16: [B, 128 nqb] the rows' intervals, padded to whole tiles
   float* part_table;        // backward: [B, H, table tiles, n_buckets]
   int table_tiles;          // query tiles per head that write part_table
   int32_t* status;
@@ -109,11 +110,12 @@ struct ScoreArgs {
 };
 
 // score_simt.cu (fp32, FFMA)
-int launch_score_fwd_simt(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
-int launch_score_bwd_simt(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
+int launch_score_fwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
+int launch_score_bwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 // score_fwd.cu (bf16, tcgen05)
 bool score_packs(int G, int Nq, bool mask, bool table);
 int score_splits(int B, int heads, int nq_tiles, int nkb);
+int launch_score_bwd_tc(const ScoreArgs& a, int d, cudaStream_t s);   // score_bwd.cu
 int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s);
 // score_plan.cu
 int launch_attn_spans(int B, int Nq, int Nk, int causal, const int32_t* docs, int n_docs, const int32_t* prefix,

@@ -127,9 +127,8 @@ void fwd_plan(ScoreArgs& a, bool packed) {
   a.splits = score_splits(a.B, packed ? a.Hkv : a.H, packed ? 1 : a.nqb, a.nkb);
 }
 
-// Backward workspace: [row_lse][row_d][part_table], 256-byte aligned pieces.
+// Backward workspace: [row_lse][row_d][row_span][part_table], 256-byte aligned pieces.
 size_t bwd_layout(ScoreArgs& a, int dtype, void* ws) {
-  (void)dtype;
   char* p = static_cast<char*>(ws);
   size_t off = 0;
   const size_t rows = static_cast<size_t>(a.B) * a.H * a.nqb * 128;
@@ -137,8 +136,12 @@ size_t bwd_layout(ScoreArgs& a, int dtype, void* ws) {
   off += align256(rows * 4);
   a.row_d = reinterpret_cast<float*>(p + off);
   off += align256(rows * 4);
+  if (dtype == CALIBATT_BF16) {
+    a.row_span = reinterpret_cast<int2*>(p + off);
+    off += align256(static_cast<size_t>(a.B) * a.nqb * 128 * 8);
+  }
   if (a.dtable != nullptr) {
-    a.table_tiles = (a.Nq + 63) / 64;
+    a.table_tiles = dtype == CALIBATT_BF16 ? a.nqb : (a.Nq + 63) / 64;
     a.part_table = reinterpret_cast<float*>(p + off);
     off += align256(static_cast<size_t>(a.B) * a.H * a.table_tiles * a.n_buckets * 4);
   }
@@ -226,7 +229,7 @@ int calibatt_score_attn_fwd(const calibatt_tensor4* q, const calibatt_tensor4* k
   a.lse = lse;
   a.status = dev_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == CALIBATT_FP32) return launch_score_fwd_simt(a, d, dtype, s);
+  if (dtype == CALIBATT_FP32) return launch_score_fwd_simt(a, d, s);
   fwd_plan(a, score_packs(a.G, Nq, a.mask != nullptr, a.table != nullptr));
   const size_t need = fwd_layout(a, d, workspace);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
@@ -282,7 +285,7 @@ int calibatt_score_attn_bwd(const calibatt_tensor4* dout, const calibatt_tensor4
                      workspace_bytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if ((rc = launch_score_rows(a, d, dtype, s))) return rc;
-  if ((rc = launch_score_bwd_simt(a, d, dtype, s))) return rc;
+  if ((rc = dtype == CALIBATT_BF16 ? launch_score_bwd_tc(a, d, s) : launch_score_bwd_simt(a, d, s))) return rc;
   return dtable != nullptr ? launch_score_table_sum(a, dtype, s) : CALIBATT_OK;
 }
 

@@ -1,0 +1,924 @@
+// score_bwd.cu -- score-modified attention backward on the tensor cores (bf16).
+//
+// Two kernels, each recomputing the scores, so that every gradient is summed
+// by one CTA in a fixed order, without atomics and without an fp32 buffer for
+// dQ:
+//   k_score_dkv  one 128-key tile of a key head: for every query tile that
+//                sees it (all G query heads) S^T = K Q^T and dP^T = V dO^T,
+//                then dV += P^T dO and dK += dS^T Q.  TMEM lanes are keys.
+//   k_score_dq   one 128-query tile: for every key tile S = Q K^T and
+//                dP = dO V^T, then dQ += dS K; and the sums of dZ by bucket.
+//                TMEM lanes are queries.
+// Both products that read a probability or dS take it as the A operand from
+// TMEM, where the softmax warps leave it as bf16 in place of the scores; the
+// other operand is the input tile as it lies in shared memory (128-byte
+// swizzle, read K-major by the first products and MN-major by the second).
+// Seven 128 x 128 x d products a tile pair instead of the five that one kernel
+// with atomics on dQ would need.
+//
+// A CTA (one per SM): warps 0-3 and 4-7 softmax, the lanes' columns split in
+// halves of 64 between the warpgroups; warp 8 TMA producer; warp 9 MMA issuer;
+// warp 10 fills the table's windows one tile ahead.  With P = exp(z - LSE)
+// known from the forward's LSE no running maximum is needed.
+#include <algorithm>
+#include <atomic>
+
+#include "score_common.cuh"
+
+namespace calibatt {
+namespace {
+
+constexpr int TILE = 128;
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;
+constexpr uint32_t kSoftmaxRegs = 208;
+constexpr uint32_t kControlRegs = 88;
+static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
+constexpr int kProducer = 8, kMma = 9, kWindow = 10;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kRowBytes = 512 + 512 + 1024;   // -LSE, -D and interval of a tile's rows
+
+template <int D>
+__device__ __forceinline__ void mma_scores(uint32_t t, uint32_t sA, uint32_t sB, uint32_t idesc) {
+  constexpr uint32_t BOX = TILE * 64 * 2;
+  if (D == 128) {
+    mma_ss_k128_w(t, sdesc_sw128(sA, 16, 1024), sdesc_sw128(sB, 16, 1024), idesc, BOX >> 4);
+  } else {
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      mma_bf16_ss_w(t, sdesc_sw128(sA + kk * 32, 16, 1024), sdesc_sw128(sB + kk * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+  }
+}
+
+// D[t] (+)= A B with A the bf16 pairs at columns [ta, ta + 32) and [ta + 64, ta + 96)
+// (the two halves of 64 columns) and B the MN-major tile at sB.
+__device__ __forceinline__ void mma_from_tmem(uint32_t t, uint32_t ta, uint32_t sB, uint32_t idesc, uint32_t accumulate) {
+  const uint64_t bd = sdesc_sw128(sB, TILE * 64 * 2, 1024);
+  mma_ts_k64_w(t, ta, bd, idesc, accumulate);
+  mma_ts_k64_w(t, ta + 64, bd + 512, idesc, 1u);
+}
+
+// Whether the table's value varies over a tile pair: some offset is nearer than the distance on its side.
+__device__ __forceinline__ bool is_near(const ScoreArgs& a, int k0, int p0) {
+  return a.table != nullptr && k0 - (p0 + TILE - 1) < a.R && k0 + TILE - 1 - p0 > -a.R;
+}
+
+// Warp 10's work for one tile pair: the table's values (and buckets) of the
+// offsets k0 - p0 - 127 ... k0 - p0 + 127.
+__device__ __forceinline__ void fill_window(const ScoreArgs& a, int h, int k0, int p0, float* win, uint8_t* bwin, bool* bad) {
+  const __nv_bfloat16* tab = reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
+  int n[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) n[x] = score_bucket(a, k0 - p0 - (TILE - 1) + x * 32 + lane_id(), bad);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    win[x * 32 + lane_id()] = __bfloat162float(tab[n[x]]) * kLog2e;
+    if (bwin != nullptr) bwin[x * 32 + lane_id()] = static_cast<uint8_t>(n[x]);
+  }
+}
+
+// ===========================================================================
+// dK, dV
+// ===========================================================================
+
+template <int D>
+struct DkvLayout {
+  static constexpr uint32_t BOX = TILE * 64 * 2;
+  static constexpr uint32_t TB = TILE * D * 2;
+  static constexpr int RING = D == 128 ? 2 : 4;   // stages of a query tile's Q, dO and row terms
+  static constexpr uint32_t OFF_K = 0;
+  static constexpr uint32_t OFF_V = TB;
+  static constexpr uint32_t OFF_Q = 2 * TB;
+  static constexpr uint32_t OFF_DO = OFF_Q + RING * TB;
+  static constexpr uint32_t OFF_ROWS = OFF_DO + RING * TB;
+  static constexpr uint32_t OFF_WIN = OFF_ROWS + RING * kRowBytes;   // float [2][256]
+  static constexpr uint32_t OFF_CTRL = OFF_WIN + 2048;
+  static constexpr uint32_t SMEM = OFF_CTRL + 1024 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+template <int RING>
+struct DkvCtrl {
+  uint64_t kv_full, ring_full[RING], ring_empty[RING];
+  uint64_t s_full, p_full, dp_full, ds_full, o_full, drain;
+  uint64_t win_full[2], win_empty[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+// Walk over the (query head, query tile) pairs that see key tile kb.
+struct QueryWalk {
+  int g, qb;
+  uint32_t word;
+  int wbase;
+};
+
+__device__ __forceinline__ uint32_t query_word(const ScoreArgs& a, int b, int hk, int kb, int g, int wbase) {
+  const int qb = wbase + lane_id();
+  bool on = false;
+  if (qb < a.nqb) {
+    const int4 r = score_tile(a, b, qb);
+    on = r.x < r.y && r.x < (kb + 1) * TILE && r.y > kb * TILE && score_kept(a, hk * a.G + g, qb, kb);
+  }
+  return __ballot_sync(0xffffffffu, on);
+}
+
+// Next pair; false at the end.
+__device__ __forceinline__ bool query_next(const ScoreArgs& a, int b, int hk, int kb, QueryWalk& w) {
+  while (w.word == 0) {
+    w.wbase += 32;
+    if (w.wbase >= a.nqb) {
+      w.wbase = 0;
+      if (++w.g >= a.G) return false;
+    }
+    w.word = query_word(a, b, hk, kb, w.g, w.wbase);
+  }
+  w.qb = w.wbase + __ffs(w.word) - 1;
+  w.word &= w.word - 1;
+  return true;
+}
+
+__device__ __forceinline__ bool query_start(const ScoreArgs& a, int b, int hk, int kb, QueryWalk& w) {
+  w.g = 0;
+  w.wbase = -32;
+  w.word = 0;
+  return query_next(a, b, hk, kb, w);
+}
+
+// Rounds 64 fp32 values of a lane to bf16 pairs in TMEM columns [t, t + 32).
+__device__ __forceinline__ void store_half(uint32_t t, const float (&x)[64]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) pk[i] = pack_bf16x2(x[c * 32 + 2 * i], x[c * 32 + 2 * i + 1]);
+    tmem_st16(t + c * 16, pk);
+  }
+}
+
+// Writes D TMEM columns of this lane, times `mul`, as one bf16 row.
+template <int COLS>
+__device__ __forceinline__ void store_row(uint32_t t, __nv_bfloat16* dst, float mul, bool live) {
+#pragma unroll
+  for (int q = 0; q < COLS / 32; ++q) {
+    uint32_t r[32];
+    tmem_ld32(t + q * 32, r);
+    tmem_ld_wait();
+    reg_fence(r);
+    if (live) {
+#pragma unroll
+      for (int v = 0; v < 4; ++v)
+        reinterpret_cast<uint4*>(dst + q * 32)[v] =
+            make_uint4(pack_bf16x2(u2f(r[8 * v + 0]) * mul, u2f(r[8 * v + 1]) * mul),
+                       pack_bf16x2(u2f(r[8 * v + 2]) * mul, u2f(r[8 * v + 3]) * mul),
+                       pack_bf16x2(u2f(r[8 * v + 4]) * mul, u2f(r[8 * v + 5]) * mul),
+                       pack_bf16x2(u2f(r[8 * v + 6]) * mul, u2f(r[8 * v + 7]) * mul));
+    }
+  }
+}
+
+template <int COLS>
+__device__ __forceinline__ void zero_row(__nv_bfloat16* dst, bool live) {
+  if (!live) return;
+#pragma unroll
+  for (int x = 0; x < COLS / 8; ++x) reinterpret_cast<uint4*>(dst)[x] = make_uint4(0, 0, 0, 0);
+}
+
+// TMEM: S^T (P^T in place) [0, 128), dP^T (dS^T in place) [128, 256), dV at
+// 256, dK at 384.  Issue order: S(0), dP(0); then per pair t, once P(t) is
+// stored, dV(t) and S(t + 1), and once dS(t) is stored, dK(t) and dP(t + 1):
+// the exponentials of pair t + 1 run while dK(t) and dP(t + 1) do, the
+// products' second half of the softmax (dS) while dV and S of the next do.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_score_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+                const __grid_constant__ ScoreArgs a) {
+  using L = DkvLayout<D>;
+  constexpr int R = L::RING;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  DkvCtrl<R>* c = reinterpret_cast<DkvCtrl<R>*>(smem + L::OFF_CTRL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // key tiles of a head side by side: they read the same Q and dO; under a
+  // causal rule the first ones, which most queries see, start first
+  const int kb = blockIdx.x % a.nkb, bh = blockIdx.x / a.nkb;
+  const int b = bh / a.Hkv, hk = bh % a.Hkv;
+  const int k0 = kb * TILE;
+
+  if (threadIdx.x == 0) {
+    mbar_init(&c->kv_full, 1);
+    for (int e = 0; e < R; ++e) {
+      mbar_init(&c->ring_full[e], 1);
+      mbar_init(&c->ring_empty[e], 1);
+    }
+    mbar_init(&c->s_full, 1);
+    mbar_init(&c->p_full, 256);
+    mbar_init(&c->dp_full, 1);
+    mbar_init(&c->ds_full, 256);
+    mbar_init(&c->o_full, 1);
+    mbar_init(&c->drain, 1);
+    for (int e = 0; e < 2; ++e) {
+      mbar_init(&c->win_full[e], 32);
+      mbar_init(&c->win_empty[e], 256);
+    }
+    c->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmDO);
+  }
+  if (warp == kMma) {
+    tmem_alloc(&c->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem_base;
+  const uint32_t tS = tmem, tP = tmem + 128, tV = tmem + 256, tK = tmem + 384;
+
+  if (warp >= 8) regs_dec<kControlRegs>();
+  if (warp == kProducer) {
+    QueryWalk w;
+    bool more = query_start(a, b, hk, kb, w), ok = true;
+    const bool any = more;
+    uint32_t t = 0;
+    const uint64_t pol = l2_policy_evict_last(), pol_kv = l2_policy_evict_first();
+    if (any) {
+      mbar_arrive_expect_tx_w(&c->kv_full, 2 * L::TB);
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) {
+        tma_load_4d_w(smem + L::OFF_K + x * L::BOX, &tmK, x * 64, k0, hk, b, &c->kv_full, pol_kv);
+        tma_load_4d_w(smem + L::OFF_V + x * L::BOX, &tmV, x * 64, k0, hk, b, &c->kv_full, pol_kv);
+      }
+    }
+    while (more) {
+      const int e = t % R;
+      ok = __all_sync(0xffffffffu, mbar_wait(&c->ring_empty[e], ((t / R) & 1) ^ 1, &c->abort, a.spin_ns));
+      if (!ok) break;
+      mbar_arrive_expect_tx_w(&c->ring_full[e], 2 * L::TB + kRowBytes);
+      const int h = hk * a.G + w.g;
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) {
+        tma_load_4d_w(smem + L::OFF_Q + e * L::TB + x * L::BOX, &tmQ, x * 64, w.qb * TILE, h, b, &c->ring_full[e], pol);
+        tma_load_4d_w(smem + L::OFF_DO + e * L::TB + x * L::BOX, &tmDO, x * 64, w.qb * TILE, h, b, &c->ring_full[e], pol);
+      }
+      uint8_t* rows = smem + L::OFF_ROWS + e * kRowBytes;
+      const size_t r0 = ((static_cast<size_t>(b) * a.H + h) * a.nqb + w.qb) * TILE;
+      bulk_load_w(rows, a.row_lse + r0, 512, &c->ring_full[e]);
+      bulk_load_w(rows + 512, a.row_d + r0, 512, &c->ring_full[e]);
+      bulk_load_w(rows + 1024, a.row_span + (static_cast<size_t>(b) * a.nqb + w.qb) * TILE, 1024, &c->ring_full[e]);
+      ++t;
+      more = query_next(a, b, hk, kb, w);
+    }
+    if (lane == 0) {
+      if (!ok) {
+        c->abort = 1;
+        report_status(a.status, CALIBATT_E_TIMEOUT);
+      }
+      // Drain: every copy issued must have landed before the CTA may exit.
+      if (any) mbar_wait(&c->kv_full, 0, nullptr, a.spin_ns);
+      for (int e = 0; e < R; ++e) {
+        const uint32_t fills = (t > static_cast<uint32_t>(e)) ? (t - 1 - e) / R + 1 : 0;
+        if (fills > 0) mbar_wait(&c->ring_full[e], (fills - 1) & 1, nullptr, a.spin_ns);
+      }
+    }
+  } else if (warp == kMma) {
+    uint32_t n = 0;
+    for (int g = 0; g < a.G; ++g)
+      for (int w = 0; w < a.nqb; w += 32) n += __popc(query_word(a, b, hk, kb, g, w));
+    constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, TILE, false);
+    constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D, true);
+    const uint32_t sK = smem_u32(smem + L::OFF_K), sV = smem_u32(smem + L::OFF_V);
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &c->abort, a.spin_ns));
+      tc_fence_after();
+      return ok;
+    };
+    auto sQ = [&](uint32_t t) { return smem_u32(smem + L::OFF_Q + (t % R) * L::TB); };
+    auto sO = [&](uint32_t t) { return smem_u32(smem + L::OFF_DO + (t % R) * L::TB); };
+    if (n > 0 && wait(&c->kv_full, 0) && wait(&c->ring_full[0], 0)) {
+      mma_scores<D>(tS, sK, sQ(0), IDESC_S);
+      mma_commit_w(&c->s_full);
+      mma_scores<D>(tP, sV, sO(0), IDESC_S);
+      mma_commit_w(&c->dp_full);
+      for (uint32_t t = 0; t < n; ++t) {
+        if (!wait(&c->p_full, t & 1)) break;
+        mma_from_tmem(tV, tS, sO(t), IDESC_O, t > 0 ? 1u : 0u);
+        if (t + 1 < n) {
+          if (!wait(&c->ring_full[(t + 1) % R], ((t + 1) / R) & 1)) break;
+          mma_scores<D>(tS, sK, sQ(t + 1), IDESC_S);
+          mma_commit_w(&c->s_full);
+        }
+        if (!wait(&c->ds_full, t & 1)) break;
+        mma_from_tmem(tK, tP, sQ(t), IDESC_O, t > 0 ? 1u : 0u);
+        mma_commit_w(&c->ring_empty[t % R]);
+        if (t + 1 < n) {
+          mma_scores<D>(tP, sV, sO(t + 1), IDESC_S);
+          mma_commit_w(&c->dp_full);
+        } else {
+          mma_commit_w(&c->o_full);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      c->abort = 1;
+      report_status(a.status, CALIBATT_E_TIMEOUT);
+    }
+    __syncwarp();
+    mma_commit_w(&c->drain);
+    mbar_wait(&c->drain, 0, nullptr, a.spin_ns);
+  } else if (warp == kWindow) {
+    if (a.table != nullptr) {
+      QueryWalk w;
+      bool bad = false, ok = true;
+      uint32_t t = 0;
+      for (bool more = query_start(a, b, hk, kb, w); more; more = query_next(a, b, hk, kb, w), ++t) {
+        const int e = t & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&c->win_empty[e], ((t >> 1) & 1) ^ 1, &c->abort, a.spin_ns));
+        if (!ok) break;
+        const int p0 = a.q_start[b] + w.qb * TILE;
+        if (is_near(a, k0, p0))
+          fill_window(a, hk * a.G + w.g, k0, p0, reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256, nullptr, &bad);
+        mbar_arrive(&c->win_full[e]);
+      }
+      if (!ok) {
+        c->abort = 1;
+        report_status(a.status, CALIBATT_E_TIMEOUT);
+      }
+      if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
+    }
+  } else if (warp < 8) {
+    regs_inc<kSoftmaxRegs>();
+    const int half = warp >> 2, w4 = warp & 3, row = w4 * 32 + lane;   // row: key of the tile
+    const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t tSh = tS + lanes + half * 64, tPh = tP + lanes + half * 64;
+    const ScoreTerms terms = score_terms(a);
+    const bool xform = a.cap > 0.f || a.slopes != nullptr || a.table != nullptr;
+    const uint64_t c2x2 = f2pack(xform ? 1.f : terms.sc, xform ? 1.f : terms.sc);
+    const int j = k0 + row;
+    bool ok = true;
+    uint32_t t = 0;
+    QueryWalk w;
+    for (bool more = query_start(a, b, hk, kb, w); more; more = query_next(a, b, hk, kb, w), ++t) {
+      const int e = t % R, h = hk * a.G + w.g;
+      const int p0 = a.q_start[b] + w.qb * TILE;
+      const int4 tr = score_tile(a, b, w.qb);
+      const bool edge = k0 < tr.z || k0 + TILE > tr.w;
+      const bool near = is_near(a, k0, p0);
+      const uint8_t* rows = smem + L::OFF_ROWS + e * kRowBytes;
+      const float4* nlse = reinterpret_cast<const float4*>(rows) + half * 16;
+      const float4* nd = reinterpret_cast<const float4*>(rows + 512) + half * 16;
+      float slope = 0.f, far = 0.f;
+      if (a.slopes != nullptr) slope = a.slopes[h] * kLog2e;
+      if (a.table != nullptr && !near) {
+        bool bad = false;
+        const int n = score_bucket(a, k0 > p0 ? a.R : -a.R, &bad);
+        far = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n]) * kLog2e;
+        if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
+      }
+      bool got = mbar_wait(&c->s_full, t & 1, &c->abort, a.spin_ns) &&
+                 mbar_wait(&c->ring_full[e], (t / R) & 1, &c->abort, a.spin_ns);
+      if (got && a.table != nullptr) got = mbar_wait(&c->win_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && edge) got = mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[64];
+      tmem_ld32(tSh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+      tmem_ld32(tSh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+      tmem_ld_wait();
+      reg_fence(r);
+      float pf[64];   // first the cap's factor, then P times it
+      if (xform) {
+        // column x: query 64 half + x, offset j - p falls with x
+        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (t & 1) * 256 + row + TILE - 1 - half * 64;
+        score_columns<-1, true>(a, terms, r, pf, slope, static_cast<float>(j - p0 - half * 64), near, wr, far);
+        if (a.table != nullptr) mbar_arrive(&c->win_empty[t & 1]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 64; ++x) pf[x] = 1.f;
+      }
+      uint32_t seen0 = 0xffffffffu, seen1 = 0xffffffffu;
+      if (edge) {
+        const int4* span = reinterpret_cast<const int4*>(rows + 1024) + half * 32;
+        seen0 = seen1 = 0;
+#pragma unroll
+        for (int x = 0; x < 64; x += 2) {
+          const int4 v = span[x / 2];
+          const uint32_t bits = (j >= v.x && j < v.y ? 1u : 0u) | (j >= v.z && j < v.w ? 2u : 0u);
+          if (x < 32) seen0 |= bits << x; else seen1 |= bits << (x - 32);
+        }
+        // Queries with a NaN or an infinity would leave it in every key's sums
+        // through a probability of 0: their rows of Q (read by S, which is
+        // complete) and of dO (read by dP, awaited above) are zeroed before
+        // the second products.  Keys that are seen get it from P or dS, which
+        // are NaN then.
+#pragma unroll
+        for (int x = 0; x < D / 64; ++x)
+          clean_box_row(smem + (half == 0 ? L::OFF_Q : L::OFF_DO) + e * L::TB + x * L::BOX + row * 128, row);
+        fence_proxy_async_smem();
+      }
+      // P, rounded to bf16 for dV, and P times the cap's factor kept for dS
+      {
+        float pv[64];
+#pragma unroll
+        for (int x = 0; x < 64; x += 4) {
+          const float4 nl = nlse[x / 4];
+          float y0, y1, y2, y3;
+          f2unpack(ffma2(f2pack(u2f(r[x]), u2f(r[x + 1])), c2x2, f2pack(nl.x, nl.y)), y0, y1);
+          f2unpack(ffma2(f2pack(u2f(r[x + 2]), u2f(r[x + 3])), c2x2, f2pack(nl.z, nl.w)), y2, y3);
+          pv[x] = ex2_approx(y0);
+          pv[x + 1] = ex2_approx(y1);
+          pv[x + 2] = ex2_approx(y2);
+          pv[x + 3] = ex2_approx(y3);
+        }
+        if (edge) {
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            if (!((x < 32 ? seen0 >> x : seen1 >> (x - 32)) & 1u)) pv[x] = 0.f;
+        }
+        store_half(tSh, pv);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&c->p_full);
+#pragma unroll
+        for (int x = 0; x < 64; ++x) pf[x] *= pv[x];
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns));
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(tPh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+      tmem_ld32(tPh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+      tmem_ld_wait();
+      reg_fence(r);
+#pragma unroll
+      for (int x = 0; x < 64; x += 4) {
+        const float4 d4 = nd[x / 4];
+        float y0, y1;
+        f2unpack(fmul2(fadd2(f2pack(u2f(r[x]), u2f(r[x + 1])), f2pack(d4.x, d4.y)), f2pack(pf[x], pf[x + 1])), y0, y1);
+        pf[x] = y0;
+        pf[x + 1] = y1;
+        f2unpack(fmul2(fadd2(f2pack(u2f(r[x + 2]), u2f(r[x + 3])), f2pack(d4.z, d4.w)), f2pack(pf[x + 2], pf[x + 3])), y0, y1);
+        pf[x + 2] = y0;
+        pf[x + 3] = y1;
+      }
+      if (edge) {
+#pragma unroll
+        for (int x = 0; x < 64; ++x)
+          if (!((x < 32 ? seen0 >> x : seen1 >> (x - 32)) & 1u)) pf[x] = 0.f;
+      }
+      store_half(tPh, pf);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&c->ds_full);
+    }
+    // ---- epilogue: warpgroup 0 writes dV, warpgroup 1 dK ---------------------
+    const bool live = j < a.Nk;
+    const Tensor4& ot = half == 0 ? a.dv : a.dk;
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(ot.p) + b * ot.sb + hk * ot.sh + static_cast<long long>(j) * ot.sn;
+    if (ok && t > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&c->o_full, 0, &c->abort, a.spin_ns));
+      tc_fence_after();
+      if (ok) store_row<D>((half == 0 ? tV : tK) + lanes, dst, half == 0 ? 1.f : a.scale, live);
+    } else if (ok) {
+      zero_row<D>(dst, live);
+    }
+    if (!ok) {
+      c->abort = 1;
+      report_status(a.status, CALIBATT_E_TIMEOUT);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+// ===========================================================================
+// dQ and the table's gradient
+// ===========================================================================
+
+template <int D>
+struct DqLayout {
+  static constexpr uint32_t BOX = TILE * 64 * 2;
+  static constexpr uint32_t TB = TILE * D * 2;
+  static constexpr int RK = D == 128 ? 3 : 4;   // K tiles: read by S(t) and by dQ(t), two pairs later
+  static constexpr int RV = D == 128 ? 1 : 2;   // V tiles: read by dP(t) alone
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_DO = TB;
+  static constexpr uint32_t OFF_K = 2 * TB;
+  static constexpr uint32_t OFF_V = OFF_K + RK * TB;
+  static constexpr uint32_t OFF_WIN = OFF_V + RV * TB;      // float [2][256]
+  static constexpr uint32_t OFF_BWIN = OFF_WIN + 2048;      // uint8 [2][256]
+  static constexpr uint32_t OFF_HIST = OFF_BWIN + 512;      // float [8 warps][256]
+  static constexpr uint32_t OFF_CTRL = OFF_HIST + 8192;
+  static constexpr uint32_t SMEM = OFF_CTRL + 1024 + 1024;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+template <int RK, int RV>
+struct DqCtrl {
+  uint64_t q_full, k_full[RK], k_empty[RK], v_full[RV], v_empty[RV];
+  uint64_t s_full[2], dp_full, ds_full, o_full, drain;
+  uint64_t win_full[2], win_empty[2];
+  uint32_t tmem_base;
+  int abort;
+};
+
+// TMEM: S of key tile t in [128 (t & 1), + 128), dS in place; dP [256, 384);
+// dQ at 384.  Issue order: S(0), dP(0), S(1); then per tile t, once dS(t) is
+// stored, dP(t + 1), dQ(t), S(t + 2): the scores are a tile ahead, so the
+// exponentials of tile t + 1 start at once, and dP(t + 1) arrives during them.
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_score_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
+               const __grid_constant__ ScoreArgs a) {
+  using L = DqLayout<D>;
+  constexpr int RK = L::RK, RV = L::RV;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  DqCtrl<RK, RV>* c = reinterpret_cast<DqCtrl<RK, RV>*>(smem + L::OFF_CTRL);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // query tiles of a head side by side (they read the same K and V), the last
+  // ones, which see most keys under a causal rule, first
+  const int qb = a.nqb - 1 - blockIdx.x % a.nqb, bh = blockIdx.x / a.nqb;
+  const int b = bh / a.H, h = bh % a.H, hk = h / a.G;
+  const int4 tr = score_tile(a, b, qb);
+  const int lo = tr.x >> 7, hi = tr.x < tr.y ? (tr.y + TILE - 1) >> 7 : lo;
+  const int p0 = a.q_start[b] + qb * TILE;
+  float* hist = reinterpret_cast<float*>(smem + L::OFF_HIST);
+
+  if (threadIdx.x == 0) {
+    mbar_init(&c->q_full, 1);
+    for (int e = 0; e < RK; ++e) {
+      mbar_init(&c->k_full[e], 1);
+      mbar_init(&c->k_empty[e], 1);
+    }
+    for (int e = 0; e < RV; ++e) {
+      mbar_init(&c->v_full[e], 1);
+      mbar_init(&c->v_empty[e], 1);
+    }
+    for (int e = 0; e < 2; ++e) {
+      mbar_init(&c->s_full[e], 1);
+      mbar_init(&c->win_full[e], 32);
+      mbar_init(&c->win_empty[e], 256);
+    }
+    mbar_init(&c->dp_full, 1);
+    mbar_init(&c->ds_full, 256);
+    mbar_init(&c->o_full, 1);
+    mbar_init(&c->drain, 1);
+    c->abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmDO);
+  }
+  if (a.dtable != nullptr)
+    for (int x = threadIdx.x; x < 8 * 256; x += kThreads) hist[x] = 0.f;
+  if (warp == kMma) {
+    tmem_alloc(&c->tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = c->tmem_base;
+  const uint32_t tP = tmem + 256, tQ = tmem + 384;
+
+  if (warp >= 8) regs_dec<kControlRegs>();
+  if (warp == kProducer) {
+    KeyWalk w;
+    bool ok = true;
+    const bool any = key_start(a, h, qb, lo, hi, w);
+    uint32_t t = 0;
+    bool loaded_v = true;   // the last tile's V copy was issued too
+    const uint64_t pol = l2_policy_evict_last(), pol_q = l2_policy_evict_first();
+    if (any) {
+      mbar_arrive_expect_tx_w(&c->q_full, 2 * L::TB);
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x) {
+        tma_load_4d_w(smem + L::OFF_Q + x * L::BOX, &tmQ, x * 64, qb * TILE, h, b, &c->q_full, pol_q);
+        tma_load_4d_w(smem + L::OFF_DO + x * L::BOX, &tmDO, x * 64, qb * TILE, h, b, &c->q_full, pol_q);
+      }
+    }
+    while (any) {
+      const int e = t % RK, v = t % RV;
+      ok = __all_sync(0xffffffffu, mbar_wait(&c->k_empty[e], ((t / RK) & 1) ^ 1, &c->abort, a.spin_ns));
+      if (!ok) break;
+      mbar_arrive_expect_tx_w(&c->k_full[e], L::TB);
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x)
+        tma_load_4d_w(smem + L::OFF_K + e * L::TB + x * L::BOX, &tmK, x * 64, w.kb * TILE, hk, b, &c->k_full[e], pol);
+      ++t;
+      loaded_v = false;
+      ok = __all_sync(0xffffffffu, mbar_wait(&c->v_empty[v], (((t - 1) / RV) & 1) ^ 1, &c->abort, a.spin_ns));
+      if (!ok) break;
+      mbar_arrive_expect_tx_w(&c->v_full[v], L::TB);
+#pragma unroll
+      for (int x = 0; x < D / 64; ++x)
+        tma_load_4d_w(smem + L::OFF_V + v * L::TB + x * L::BOX, &tmV, x * 64, w.kb * TILE, hk, b, &c->v_full[v], pol);
+      loaded_v = true;
+      if (w.next < 0) break;
+      key_next(a, h, qb, w);
+    }
+    if (lane == 0) {
+      if (!ok) {
+        c->abort = 1;
+        report_status(a.status, CALIBATT_E_TIMEOUT);
+      }
+      // Drain: every copy issued must have landed before the CTA may exit.
+      if (any) mbar_wait(&c->q_full, 0, nullptr, a.spin_ns);
+      const uint32_t tv = loaded_v ? t : t - 1;
+      for (int e = 0; e < RK; ++e) {
+        const uint32_t fills = (t > static_cast<uint32_t>(e)) ? (t - 1 - e) / RK + 1 : 0;
+        if (fills > 0) mbar_wait(&c->k_full[e], (fills - 1) & 1, nullptr, a.spin_ns);
+      }
+      for (int e = 0; e < RV; ++e) {
+        const uint32_t fills = (tv > static_cast<uint32_t>(e)) ? (tv - 1 - e) / RV + 1 : 0;
+        if (fills > 0) mbar_wait(&c->v_full[e], (fills - 1) & 1, nullptr, a.spin_ns);
+      }
+    }
+  } else if (warp == kMma) {
+    uint32_t n = 0;
+    if (a.mask == nullptr) {
+      n = max(0, hi - lo);
+    } else {
+      for (int w = lo; w < hi; w += 32) n += __popc(__ballot_sync(0xffffffffu, w + lane < hi && score_kept(a, h, qb, w + lane)));
+    }
+    constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, TILE, false);
+    constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D, true);
+    const uint32_t sQ = smem_u32(smem + L::OFF_Q), sO = smem_u32(smem + L::OFF_DO);
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar, parity, &c->abort, a.spin_ns));
+      tc_fence_after();
+      return ok;
+    };
+    auto sK = [&](uint32_t t) { return smem_u32(smem + L::OFF_K + (t % RK) * L::TB); };
+    auto scores = [&](uint32_t t) {
+      if (!wait(&c->k_full[t % RK], (t / RK) & 1)) return false;
+      mma_scores<D>(tmem + (t & 1) * 128, sQ, sK(t), IDESC_S);
+      mma_commit_w(&c->s_full[t & 1]);
+      return true;
+    };
+    auto grads = [&](uint32_t t) {
+      if (!wait(&c->v_full[t % RV], (t / RV) & 1)) return false;
+      mma_scores<D>(tP, sO, smem_u32(smem + L::OFF_V + (t % RV) * L::TB), IDESC_S);
+      mma_commit_w(&c->dp_full);
+      mma_commit_w(&c->v_empty[t % RV]);
+      return true;
+    };
+    if (n > 0 && wait(&c->q_full, 0) && scores(0) && grads(0) && (n == 1 || scores(1))) {
+      for (uint32_t t = 0; t < n; ++t) {
+        if (!wait(&c->ds_full, t & 1)) break;
+        if (t + 1 < n && !grads(t + 1)) break;
+        mma_from_tmem(tQ, tmem + (t & 1) * 128, sK(t), IDESC_O, t > 0 ? 1u : 0u);
+        mma_commit_w(&c->k_empty[t % RK]);
+        if (t + 1 == n) mma_commit_w(&c->o_full);
+        if (t + 2 < n && !scores(t + 2)) break;
+      }
+    }
+    if (!ok && lane == 0) {
+      c->abort = 1;
+      report_status(a.status, CALIBATT_E_TIMEOUT);
+    }
+    __syncwarp();
+    mma_commit_w(&c->drain);
+    mbar_wait(&c->drain, 0, nullptr, a.spin_ns);
+  } else if (warp == kWindow) {
+    if (a.table != nullptr) {
+      KeyWalk w;
+      bool bad = false, ok = true;
+      uint32_t t = 0;
+      for (bool more = key_start(a, h, qb, lo, hi, w); more; ++t) {
+        const int e = t & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&c->win_empty[e], ((t >> 1) & 1) ^ 1, &c->abort, a.spin_ns));
+        if (!ok) break;
+        if (is_near(a, w.kb * TILE, p0))
+          fill_window(a, h, w.kb * TILE, p0, reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256,
+                      smem + L::OFF_BWIN + e * 256, &bad);
+        mbar_arrive(&c->win_full[e]);
+        more = w.next >= 0;
+        if (more) key_next(a, h, qb, w);
+      }
+      if (!ok) {
+        c->abort = 1;
+        report_status(a.status, CALIBATT_E_TIMEOUT);
+      }
+      if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
+    }
+  } else if (warp < 8) {
+    regs_inc<kSoftmaxRegs>();
+    const int half = warp >> 2, w4 = warp & 3, row = w4 * 32 + lane;   // row: query of the tile
+    const int i = qb * TILE + row;
+    const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
+    const uint32_t tPh = tP + lanes + half * 64;
+    const ScoreTerms terms = score_terms(a);
+    const bool xform = a.cap > 0.f || a.slopes != nullptr || a.table != nullptr;
+    const uint64_t c2x2 = f2pack(xform ? 1.f : terms.sc, xform ? 1.f : terms.sc);
+    const int2 vis = score_row(a, b, i);
+    const size_t r0 = (static_cast<size_t>(b) * a.H + h) * a.nqb * TILE + i;
+    const float nlse = a.row_lse[r0], nd = a.row_d[r0];
+    const uint64_t nlse2 = f2pack(nlse, nlse), nd2 = f2pack(nd, nd);
+    const float slope = a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
+    float far_lo = 0.f, far_hi = 0.f, sum_lo = 0.f, sum_hi = 0.f;
+    int n_lo = 0, n_hi = 0;
+    if (a.table != nullptr) {
+      bool bad = false;
+      const __nv_bfloat16* tab = reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
+      n_lo = score_bucket(a, -a.R, &bad);
+      n_hi = score_bucket(a, a.R, &bad);
+      far_lo = __bfloat162float(tab[n_lo]) * kLog2e;
+      far_hi = __bfloat162float(tab[n_hi]) * kLog2e;
+      if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
+    }
+    bool ok = true;
+    uint32_t t = 0;
+    KeyWalk w;
+    for (bool more = key_start(a, h, qb, lo, hi, w); more; ++t) {
+      const int k0 = w.kb * TILE;
+      const uint32_t tSh = tmem + (t & 1) * 128 + lanes + half * 64;
+      const bool edge = k0 < tr.z || k0 + TILE > tr.w;
+      const bool near = is_near(a, k0, p0);
+      bool got = mbar_wait(&c->s_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && a.table != nullptr) got = mbar_wait(&c->win_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && edge) got = mbar_wait(&c->k_full[t % RK], (t / RK) & 1, &c->abort, a.spin_ns);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[64];
+      tmem_ld32(tSh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+      tmem_ld32(tSh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+      tmem_ld_wait();
+      reg_fence(r);
+      float f[64];
+      if (xform) {
+        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (t & 1) * 256 + TILE - 1 - row + half * 64;
+        score_columns<1, true>(a, terms, r, f, slope, static_cast<float>(k0 + half * 64 - p0 - row), near, wr,
+                               k0 > p0 ? far_hi : far_lo);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 64; ++x) f[x] = 1.f;
+      }
+      if (edge && half < D / 64) {
+        // Keys with a NaN or an infinity: zeroed before dQ reads them (S, which
+        // is complete, has made a visible one's dS NaN).
+        clean_box_row(smem + L::OFF_K + (t % RK) * L::TB + half * L::BOX + row * 128, row);
+        fence_proxy_async_smem();
+      }
+      float p[64];
+#pragma unroll
+      for (int x = 0; x < 64; x += 2) {
+        float y0, y1;
+        f2unpack(ffma2(f2pack(u2f(r[x]), u2f(r[x + 1])), c2x2, nlse2), y0, y1);
+        p[x] = ex2_approx(y0);
+        p[x + 1] = ex2_approx(y1);
+      }
+      ok = __all_sync(0xffffffffu, mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns));
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld32(tPh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+      tmem_ld32(tPh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+      tmem_ld_wait();
+      reg_fence(r);
+#pragma unroll
+      for (int x = 0; x < 64; x += 2)
+        f2unpack(fmul2(fadd2(f2pack(u2f(r[x]), u2f(r[x + 1])), nd2), f2pack(p[x], p[x + 1])), p[x], p[x + 1]);
+      if (edge) {
+        const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;
+#pragma unroll
+        for (int x = 0; x < 64; ++x)
+          if (x < e0 || x >= e1) p[x] = f[x] = 0.f;   // the factor of a masked score may be NaN
+      }
+      if (a.dtable != nullptr) {   // p is dZ
+        if (near) {
+          // Sums along the diagonals (one offset each) by passing a running
+          // sum from row to row: after column x lane 31 holds the sum of the
+          // diagonal that ends in it; 31 more steps drain the others.  Runs of
+          // offsets of one bucket are added up before the warp's own
+          // accumulators are touched, so the order is fixed.
+          const uint8_t* bw = smem + L::OFF_BWIN + (t & 1) * 256 + half * 64 + 96 - w4 * 32;
+          float* acc = hist + warp * 256;
+          float diag = 0.f, run = 0.f;
+          int cur = bw[0];
+          auto add = [&](int x) {
+            const int n = bw[x];
+            if (n != cur) {
+              if (lane == 31) acc[cur] += run;
+              run = 0.f;
+              cur = n;
+            }
+            run += diag;
+          };
+#pragma unroll
+          for (int x = 0; x < 64; ++x) {
+            const float up = __shfl_up_sync(0xffffffffu, diag, 1);
+            diag = p[x] + (lane == 0 ? 0.f : up);
+            add(x);
+          }
+#pragma unroll 1
+          for (int x = 64; x < 95; ++x) {
+            const float up = __shfl_up_sync(0xffffffffu, diag, 1);
+            diag = lane == 0 ? 0.f : up;
+            add(x);
+          }
+          if (lane == 31) acc[cur] += run;
+          __syncwarp();
+        } else {
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            s0 += p[x];
+            s1 += p[x + 1];
+          }
+          if (k0 > p0) sum_hi += s0 + s1; else sum_lo += s0 + s1;
+        }
+      }
+      if (a.table != nullptr) mbar_arrive(&c->win_empty[t & 1]);
+#pragma unroll
+      for (int x = 0; x < 64; ++x) p[x] *= f[x];
+      store_half(tSh, p);
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&c->ds_full);
+      more = w.next >= 0;
+      if (more) key_next(a, h, qb, w);
+    }
+    // ---- epilogue: each warpgroup writes half of dQ's columns ----------------
+    const bool live = i < a.Nq;
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.dq.p) + b * a.dq.sb + h * a.dq.sh +
+                         static_cast<long long>(i) * a.dq.sn + half * (D / 2);
+    if (ok && t > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&c->o_full, 0, &c->abort, a.spin_ns));
+      tc_fence_after();
+      if (ok) store_row<D / 2>(tQ + lanes + half * (D / 2), dst, a.scale, live);
+    } else if (ok) {
+      zero_row<D / 2>(dst, live);
+    }
+    if (!ok) {
+      c->abort = 1;
+      report_status(a.status, CALIBATT_E_TIMEOUT);
+    }
+    if (a.dtable != nullptr) {
+#pragma unroll
+      for (int m = 16; m > 0; m >>= 1) {
+        sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, m);
+        sum_hi += __shfl_xor_sync(0xffffffffu, sum_hi, m);
+      }
+      if (lane == 31) {
+        hist[warp * 256 + n_lo] += sum_lo;
+        hist[warp * 256 + n_hi] += sum_hi;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (a.dtable != nullptr) {
+    float* dst = a.part_table + ((static_cast<size_t>(b) * a.H + h) * a.table_tiles + qb) * a.n_buckets;
+    for (int n = threadIdx.x; n < a.n_buckets; n += kThreads) {
+      float s = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) s += hist[x * 256 + n];
+      dst[n] = s;
+    }
+  }
+  if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int D>
+int launch(const ScoreArgs& a, cudaStream_t s) {
+  CUtensorMap tq, tk, tv, to;
+  int rc;
+  if ((rc = make_tmap4_bf16(&tq, a.q, a.B, a.H, a.Nq, D, TILE, 1))) return rc;
+  if ((rc = make_tmap4_bf16(&tk, a.k, a.B, a.Hkv, a.Nk, D, TILE, 1))) return rc;
+  if ((rc = make_tmap4_bf16(&tv, a.v, a.B, a.Hkv, a.Nk, D, TILE, 1))) return rc;
+  if ((rc = make_tmap4_bf16(&to, a.dout, a.B, a.H, a.Nq, D, TILE, 1))) return rc;
+  const long long nk = static_cast<long long>(a.B) * a.Hkv * a.nkb, nq = static_cast<long long>(a.B) * a.H * a.nqb;
+  if (nk >= (1ll << 31) || nq >= (1ll << 31)) return set_error(CALIBATT_E_UNSUPPORTED, "too many tiles");
+  static std::atomic<bool> done_kv[kMaxDevices], done_q[kMaxDevices];
+  auto dkv = k_score_dkv<D>;
+  auto dq = k_score_dq<D>;
+  if ((rc = configure_kernel(reinterpret_cast<const void*>(dkv), done_kv, DkvLayout<D>::SMEM, kLaunchRegs, "k_score_dkv")))
+    return rc;
+  if ((rc = configure_kernel(reinterpret_cast<const void*>(dq), done_q, DqLayout<D>::SMEM, kLaunchRegs, "k_score_dq")))
+    return rc;
+  dkv<<<static_cast<unsigned>(nk), kThreads, DkvLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
+  dq<<<static_cast<unsigned>(nq), kThreads, DqLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
+  count_launch(2);
+  return check_launch("k_score_bwd");
+}
+
+}  // namespace
+
+int launch_score_bwd_tc(const ScoreArgs& a, int d, cudaStream_t s) { return d == 128 ? launch<128>(a, s) : launch<64>(a, s); }
+
+}  // namespace calibatt

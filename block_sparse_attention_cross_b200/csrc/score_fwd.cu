@@ -25,7 +25,6 @@
 // the launch), HBM for few queries.
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "score_common.cuh"
 
@@ -72,28 +71,6 @@ struct Ctrl {
   uint32_t bad[2][4];   // keys of a slot's V tile that hold a non-finite value
 };
 
-template <int V>
-using IntC = std::integral_constant<int, V>;
-
-__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
-__device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
-__device__ __forceinline__ float rcp_approx(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ void tma_load_4d_w(void* dst, const CUtensorMap* tm, int x, int n, int h, int b, uint64_t* bar,
-                                              uint64_t policy) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}\n" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(n), "r"(h), "r"(b), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-
 struct FwdArgs {
   ScoreArgs a;
   int Hx;       // heads of the tile grid: Hkv where the G heads share a tile, else H
@@ -102,13 +79,9 @@ struct FwdArgs {
   int T;        // tiles
 };
 
-// One tile of the walk and its current key tile.  Every role evaluates the
-// same data, warp-collectively, so all agree.
-struct Walk {
+// One tile of the walk and its current key tile.
+struct Walk : KeyWalk {
   int b, hx, qb, sp;
-  int kb, next, hi;      // current and next kept key tile (-1: none), end of the range
-  uint32_t word;         // mask: kept tiles after `next` in the 32 tiles from wbase on
-  int wbase;
 };
 
 // Order of the tiles: heads in groups whose K and V fit well into L2, and
@@ -128,23 +101,6 @@ __device__ __forceinline__ void tile_at(const FwdArgs& f, int t, Walk& w) {
   w.hx = bh % f.Hx;
 }
 
-__device__ __forceinline__ int walk_find(const FwdArgs& f, Walk& w) {
-  while (w.word == 0) {
-    w.wbase += 32;
-    if (w.wbase >= w.hi) return -1;
-    const int kb = w.wbase + lane_id();
-    w.word = __ballot_sync(0xffffffffu, kb < w.hi && score_kept(f.a, w.hx, w.qb, kb));
-  }
-  const int kb = w.wbase + __ffs(w.word) - 1;
-  w.word &= w.word - 1;
-  return kb;
-}
-
-__device__ __forceinline__ int walk_after(const FwdArgs& f, Walk& w, int kb) {
-  if (f.a.mask != nullptr) return walk_find(f, w);
-  return kb + 1 < w.hi ? kb + 1 : -1;
-}
-
 // Starts tile t; returns whether it has a key tile.
 __device__ __forceinline__ bool walk_start(const FwdArgs& f, int t, Walk& w) {
   tile_at(f, t, w);
@@ -157,15 +113,7 @@ __device__ __forceinline__ bool walk_start(const FwdArgs& f, int t, Walk& w) {
     w.hi = min(w.hi, lo + per);
   }
   if (r.x >= r.y) w.hi = lo;
-  w.word = 0;
-  if (f.a.mask != nullptr) {
-    w.wbase = lo - 32;
-    w.kb = walk_find(f, w);
-  } else {
-    w.kb = lo < w.hi ? lo : -1;
-  }
-  w.next = w.kb < 0 ? -1 : walk_after(f, w, w.kb);
-  return w.kb >= 0;
+  return key_start(f.a, w.hx, w.qb, lo, w.hi, w);
 }
 
 // The producer's and the MMA warp's position: key tiles of this slot's
@@ -190,8 +138,7 @@ __device__ __forceinline__ void cursor_seek(const FwdArgs& f, Cursor& c, int str
 __device__ __forceinline__ void cursor_next(const FwdArgs& f, Cursor& c, int stride) {
   if (c.w.next >= 0) {
     c.first = false;
-    c.w.kb = c.w.next;
-    c.w.next = walk_after(f, c.w, c.w.kb);
+    key_next(f.a, c.w.hx, c.w.qb, c.w);
   } else {
     c.t += stride;
     cursor_seek(f, c, stride);
@@ -396,8 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the exponential's FFMA; otherwise the transforms apply it.
     const bool xform = a.cap > 0.f || a.slopes != nullptr || a.table != nullptr;
     const float c2 = xform ? 1.f : a.scale * kLog2e;
-    const float capA = a.cap * kLog2e;
-    const float kcap = a.cap > 0.f ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+    const ScoreTerms terms = score_terms(a);
     const uint64_t c2x2 = f2pack(c2, c2);
     uint32_t gb = 0;
     int tiles = 0;
@@ -485,30 +431,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(t_s + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[q4 * 32]));
         tmem_ld_wait();
         reg_fence(r);
-        // cap tanh(x) = cap - 2 cap / (1 + e^(2x)): exact at both ends, and
-        // the MUFU's relative errors stay 1e-7 of the cap
-        if (a.cap > 0.f) {
-#pragma unroll
-          for (int x = 0; x < TILE; ++x)
-            r[x] = f2u(fmaf(-2.f * capA, rcp_approx(1.f + ex2_approx(u2f(r[x]) * kcap)), capA));
-        } else if (xform) {
-          const float sc = a.scale * kLog2e;
-#pragma unroll
-          for (int x = 0; x < TILE; ++x) r[x] = f2u(u2f(r[x]) * sc);
-        }
-        if (a.slopes != nullptr) {
-          const float d0 = static_cast<float>(k0 - p);
-#pragma unroll
-          for (int x = 0; x < TILE; ++x) r[x] = f2u(fmaf(-slope, fabsf(d0 + x), u2f(r[x])));
-        }
-        if (near) {
+        if (xform) {
           const float* wr = win + (a.packed ? min(row / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
-#pragma unroll
-          for (int x = 0; x < TILE; ++x) r[x] = f2u(u2f(r[x]) + wr[x]);
-        } else if (a.table != nullptr) {
-          const float far = k0 > p1 ? far_hi : far_lo;
-#pragma unroll
-          for (int x = 0; x < TILE; ++x) r[x] = f2u(u2f(r[x]) + far);
+          float none[TILE];
+          score_columns<1, false>(a, terms, r, none, slope, static_cast<float>(k0 - p), near, wr,
+                                  k0 > p1 ? far_hi : far_lo);
         }
         if (edge) {
           // keys outside the row's interval
@@ -524,26 +451,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                           mbar_wait(&c->ring_full[slot][ge % R], (ge / R) & 1, &c->abort, a.spin_ns));
           if (!ok) break;
           uint8_t* vrow = smem + L::OFF_RING + (slot * R + ge % R) * L::TBYTES + row * 128;
-          uint32_t nonfinite = 0;
+          bool bad = false;
 #pragma unroll
-          for (int x = 0; x < D / 64; ++x)
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch) {
-              const uint4 u = *reinterpret_cast<const uint4*>(vrow + x * L::BOX + ((ch ^ (row & 7)) << 4));
-              // an exponent of all ones carries into the sign's place
-              nonfinite |= ((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
-                           ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u);
-            }
-          const bool bad = (nonfinite & 0x80008000u) != 0;
+          for (int x = 0; x < D / 64; ++x) bad |= clean_box_row(vrow + x * L::BOX, row);
           const uint32_t bw = __ballot_sync(0xffffffffu, bad);
           if (lane == 0) c->bad[slot][w4] = bw;
-          if (bad) {
-            const uint4 z = make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int x = 0; x < D / 64; ++x)
-#pragma unroll
-              for (int ch = 0; ch < 8; ++ch) *reinterpret_cast<uint4*>(vrow + x * L::BOX + (ch << 4)) = z;
-          }
           fence_proxy_async_smem();
           if (!(ok = slot_sync())) break;
 #pragma unroll
@@ -624,8 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&c->p_full[slot]);
         if (w.next < 0) { ++gb; break; }
-        w.kb = w.next;
-        w.next = walk_after(f, w, w.kb);
+        key_next(a, w.hx, w.qb, w);
       }
       if (!ok) break;
       // ---- epilogue: O / l, LSE.  As in the block-sparse forward, the

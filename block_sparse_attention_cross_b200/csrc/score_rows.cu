@@ -9,6 +9,8 @@ namespace {
 // it: +inf where the row sees nothing (every probability becomes 0), NaN where
 // D is not finite (so that a row with a non-finite dO or O marks every
 // gradient it enters).  One warp a row: reads dO and O once, DRAM-bound.
+// The tensor-core kernels (bf16) add both terms to packed pairs: they get
+// -log2(e) LSE and -D, and the rows' intervals padded to whole tiles.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) k_score_rows(const ScoreArgs a) {
   const long long rows = 128ll * a.nqb;
@@ -40,8 +42,9 @@ __global__ void __launch_bounds__(256) k_score_rows(const ScoreArgs a) {
     else if (!isfinite(sum)) lse = NAN;
   }
   if (lane == 0) {
-    a.row_lse[w] = lse;
-    a.row_d[w] = sum;
+    a.row_lse[w] = sizeof(T) == 2 ? -kLog2e * lse : lse;
+    a.row_d[w] = sizeof(T) == 2 ? -sum : sum;
+    if (sizeof(T) == 2 && h == 0) a.row_span[b * rows + i] = r;
   }
 }
 

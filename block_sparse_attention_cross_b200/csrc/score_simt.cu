@@ -22,27 +22,18 @@ constexpr int PS = BT + 4;      // row pitch of a stored score tile
 template <int D>
 constexpr int PD = D + 4;       // row pitch of a stored input tile (16-byte aligned rows)
 
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float x, float y, float z, float w) {
   *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float x, float y, float z, float w) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(x, y), pack_bf16x2(z, w));
-}
 
 // Rows [r0, r0 + 64) of one head into shared memory, zero past n.
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void load_tile(float* dst, const Tensor4& t, int b, int h, int r0, int n) {
-  const T* src = reinterpret_cast<const T*>(t.p) + b * t.sb + h * t.sh;
+  const float* src = reinterpret_cast<const float*>(t.p) + b * t.sb + h * t.sh;
   for (int x = threadIdx.x; x < BT * D / 4; x += kThreads) {
     const int r = x / (D / 4), c = x % (D / 4) * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < n) v = load4(src + (r0 + r) * t.sn + c);
+    if (r0 + r < n) v = *reinterpret_cast<const float4*>(src + (r0 + r) * t.sn + c);
     *reinterpret_cast<float4*>(dst + r * PD<D> + c) = v;
   }
 }
@@ -125,7 +116,6 @@ __device__ __forceinline__ void clean_rows(float* X, int* bad) {
 }
 
 // z of one pair, and the cap's tanh in *th (0 without a cap).
-template <typename T>
 __device__ __forceinline__ float score_of(const ScoreArgs& a, int h, float dot, int off, float* th, bool* bad) {
   float z = dot * a.scale;
   *th = 0.f;
@@ -135,7 +125,7 @@ __device__ __forceinline__ float score_of(const ScoreArgs& a, int h, float dot, 
   }
   if (a.slopes != nullptr) z -= a.slopes[h] * fabsf(static_cast<float>(off));
   if (a.table != nullptr)
-    z += ld_elem(reinterpret_cast<const T*>(a.table) + static_cast<size_t>(h) * a.n_buckets + score_bucket(a, off, bad));
+    z += reinterpret_cast<const float*>(a.table)[static_cast<size_t>(h) * a.n_buckets + score_bucket(a, off, bad)];
   return z;
 }
 
@@ -145,7 +135,7 @@ struct SimtSmem {
   static constexpr int SC = BT * PS;      // floats of a score tile
 };
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) {
   using S = SimtSmem<D>;
   extern __shared__ __align__(16) float sm[];
@@ -168,13 +158,13 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
   }
-  load_tile<T, D>(sQ, a.q, b, h, q0, a.Nq);
+  load_tile<D>(sQ, a.q, b, h, q0, a.Nq);
   for (int k0 = t.x & ~(BT - 1); k0 < t.y; k0 += BT) {
     if (!score_kept(a, h, qb, k0 >> 7)) continue;
     const bool edge = k0 < t.z || k0 + BT > t.w;
     __syncthreads();
-    load_tile<T, D>(sK, a.k, b, hk, k0, a.Nk);
-    load_tile<T, D>(sV, a.v, b, hk, k0, a.Nk);
+    load_tile<D>(sK, a.k, b, hk, k0, a.Nk);
+    load_tile<D>(sV, a.v, b, hk, k0, a.Nk);
     __syncthreads();
     if (edge) clean_rows<D>(sV, bad_row);
     float s[4][4] = {};
@@ -188,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
         const int col = k0 + tx + 16 * j;
         float th;
         const bool see = col >= vis[i].x && col < vis[i].y;
-        s[i][j] = see ? score_of<T>(a, h, s[i][j], col - (qs + q0 + ty * 4 + i), &th, &bad) : -INFINITY;
+        s[i][j] = see ? score_of(a, h, s[i][j], col - (qs + q0 + ty * 4 + i), &th, &bad) : -INFINITY;
         if (edge && see && bad_row[tx + 16 * j]) nan_row[i] = true;
         mx = fmaxf(mx, s[i][j]);
       }
@@ -221,7 +211,7 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
     const int r = q0 + ty * 4 + i;
     if (r >= a.Nq) continue;
     const float inv = (any & 0xffffu) ? NAN : l[i] == 0.f ? 0.f : 1.f / l[i];
-    T* dst = reinterpret_cast<T*>(a.o.p) + b * a.o.sb + h * a.o.sh + r * a.o.sn;
+    float* dst = reinterpret_cast<float*>(a.o.p) + b * a.o.sb + h * a.o.sh + r * a.o.sn;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
       store4(dst + tx * 4 + 64 * c, o[i][c * 4] * inv, o[i][c * 4 + 1] * inv, o[i][c * 4 + 2] * inv, o[i][c * 4 + 3] * inv);
@@ -232,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
 
 // P and the two forms of dS of one score tile: dZ = P (dP - D) (what the bias
 // gets) and dS = dZ (1 - tanh^2) scale (what the dot product gets).
-template <typename T, int D>
+template <int D>
 __device__ __forceinline__ void grad_tile(const ScoreArgs& a, int h, int q0, int k0, int qs, const int2 (&vis)[4],
                                           const float (&lse)[4], const float (&dd)[4], const float (&s)[4][4],
                                           const float (&dp)[4][4], int ty, int tx, float* sP, float* sZ, float* sS,
@@ -244,7 +234,7 @@ __device__ __forceinline__ void grad_tile(const ScoreArgs& a, int h, int q0, int
       const int col = k0 + tx + 16 * j, at = (ty * 4 + i) * PS + tx + 16 * j;
       float th, p = 0.f, dz = 0.f;
       if (col >= vis[i].x && col < vis[i].y) {
-        const float z = score_of<T>(a, h, s[i][j], col - (qs + q0 + ty * 4 + i), &th, bad);
+        const float z = score_of(a, h, s[i][j], col - (qs + q0 + ty * 4 + i), &th, bad);
         p = expf(z - lse[i]);
         dz = p * (dp[i][j] - dd[i]);
       } else {
@@ -256,7 +246,7 @@ __device__ __forceinline__ void grad_tile(const ScoreArgs& a, int h, int q0, int
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
   using S = SimtSmem<D>;
   extern __shared__ __align__(16) float sm[];
@@ -281,19 +271,19 @@ __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
   }
   if (a.dtable != nullptr)
     for (int n = threadIdx.x; n < a.n_buckets; n += kThreads) acc_t[n] = 0.f;
-  load_tile<T, D>(sQ, a.q, b, h, q0, a.Nq);
-  load_tile<T, D>(sO, a.dout, b, h, q0, a.Nq);
+  load_tile<D>(sQ, a.q, b, h, q0, a.Nq);
+  load_tile<D>(sO, a.dout, b, h, q0, a.Nq);
   for (int k0 = t.x & ~(BT - 1); k0 < t.y; k0 += BT) {
     if (!score_kept(a, h, qb, k0 >> 7)) continue;
     const bool edge = k0 < t.z || k0 + BT > t.w;
     __syncthreads();
-    load_tile<T, D>(sK, a.k, b, hk, k0, a.Nk);
-    load_tile<T, D>(sV, a.v, b, hk, k0, a.Nk);
+    load_tile<D>(sK, a.k, b, hk, k0, a.Nk);
+    load_tile<D>(sV, a.v, b, hk, k0, a.Nk);
     __syncthreads();
     float s[4][4] = {}, dp[4][4] = {};
     dot_tile<D>(s, sQ, sK, ty, tx);
     dot_tile<D>(dp, sO, sV, ty, tx);
-    grad_tile<T, D>(a, h, q0, k0, qs, vis, lse, dd, s, dp, ty, tx, nullptr, a.dtable ? sZ : nullptr, sS, &bad);
+    grad_tile<D>(a, h, q0, k0, qs, vis, lse, dd, s, dp, ty, tx, nullptr, a.dtable ? sZ : nullptr, sS, &bad);
     __syncthreads();
     if (edge) {
       clean_rows<D>(sK, bad_row);   // the scores that read them are formed: a visible one is in dS as NaN
@@ -322,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
   for (int i = 0; i < 4; ++i) {
     const int r = q0 + ty * 4 + i;
     if (r >= a.Nq) continue;
-    T* dst = reinterpret_cast<T*>(a.dq.p) + b * a.dq.sb + h * a.dq.sh + r * a.dq.sn;
+    float* dst = reinterpret_cast<float*>(a.dq.p) + b * a.dq.sb + h * a.dq.sh + r * a.dq.sn;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
       store4(dst + tx * 4 + 64 * c, dq[i][c * 4], dq[i][c * 4 + 1], dq[i][c * 4 + 2], dq[i][c * 4 + 3]);
@@ -334,7 +324,7 @@ __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
   }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) {
   using S = SimtSmem<D>;
   extern __shared__ __align__(16) float sm[];
@@ -345,8 +335,8 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
   const int qs = a.q_start[b];
   float dk[4][D / 16] = {}, dv[4][D / 16] = {};
   bool bad = false;
-  load_tile<T, D>(sK, a.k, b, hk, k0, a.Nk);
-  load_tile<T, D>(sV, a.v, b, hk, k0, a.Nk);
+  load_tile<D>(sK, a.k, b, hk, k0, a.Nk);
+  load_tile<D>(sV, a.v, b, hk, k0, a.Nk);
   for (int g = 0; g < a.G; ++g) {
     const int h = hk * a.G + g;
     for (int q0 = 0; q0 < a.Nq; q0 += BT) {
@@ -355,8 +345,8 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
       if (t.x >= k0 + BT || t.y <= k0 || !score_kept(a, h, qb, k0 >> 7)) continue;
       const bool edge = k0 < t.z || k0 + BT > t.w;
       __syncthreads();
-      load_tile<T, D>(sQ, a.q, b, h, q0, a.Nq);
-      load_tile<T, D>(sO, a.dout, b, h, q0, a.Nq);
+      load_tile<D>(sQ, a.q, b, h, q0, a.Nq);
+      load_tile<D>(sO, a.dout, b, h, q0, a.Nq);
       int2 vis[4];
       float lse[4], dd[4];
       const size_t r0 = (static_cast<size_t>(b) * a.H + h) * a.nqb * 128 + q0;
@@ -370,7 +360,7 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
       float s[4][4] = {}, dp[4][4] = {};
       dot_tile<D>(s, sQ, sK, ty, tx);
       dot_tile<D>(dp, sO, sV, ty, tx);
-      grad_tile<T, D>(a, h, q0, k0, qs, vis, lse, dd, s, dp, ty, tx, sP, nullptr, sS, &bad);
+      grad_tile<D>(a, h, q0, k0, qs, vis, lse, dd, s, dp, ty, tx, sP, nullptr, sS, &bad);
       __syncthreads();
       if (edge) {
         clean_rows<D>(sQ, bad_row);
@@ -386,8 +376,8 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
   for (int i = 0; i < 4; ++i) {
     const int r = k0 + ty * 4 + i;
     if (r >= a.Nk) continue;
-    T* pk = reinterpret_cast<T*>(a.dk.p) + b * a.dk.sb + hk * a.dk.sh + r * a.dk.sn;
-    T* pv = reinterpret_cast<T*>(a.dv.p) + b * a.dv.sb + hk * a.dv.sh + r * a.dv.sn;
+    float* pk = reinterpret_cast<float*>(a.dk.p) + b * a.dk.sb + hk * a.dk.sh + r * a.dk.sn;
+    float* pv = reinterpret_cast<float*>(a.dv.p) + b * a.dv.sb + hk * a.dv.sh + r * a.dv.sn;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       store4(pk + tx * 4 + 64 * c, dk[i][c * 4], dk[i][c * 4 + 1], dk[i][c * 4 + 2], dk[i][c * 4 + 3]);
@@ -405,39 +395,32 @@ int set_smem(K kern, size_t bytes) {
   return CALIBATT_OK;
 }
 
-template <typename T, int D>
+template <int D>
 int fwd(const ScoreArgs& a, cudaStream_t s) {
   using S = SimtSmem<D>;
   const size_t smem = (3 * S::IN + S::SC) * sizeof(float);
-  if (int rc = set_smem(k_score_fwd_simt<T, D>, smem)) return rc;
-  k_score_fwd_simt<T, D><<<dim3((a.Nq + BT - 1) / BT, a.H, a.B), kThreads, smem, s>>>(a);
+  if (int rc = set_smem(k_score_fwd_simt<D>, smem)) return rc;
+  k_score_fwd_simt<D><<<dim3((a.Nq + BT - 1) / BT, a.H, a.B), kThreads, smem, s>>>(a);
   count_launch();
   return check_launch("k_score_fwd_simt");
 }
 
-template <typename T, int D>
+template <int D>
 int bwd(const ScoreArgs& a, cudaStream_t s) {
   using S = SimtSmem<D>;
   const size_t smem_q = (4 * S::IN + 2 * S::SC + 2 * BT + a.n_buckets) * sizeof(float);
   const size_t smem_k = (4 * S::IN + 2 * S::SC) * sizeof(float);
-  if (int rc = set_smem(k_score_dq_simt<T, D>, smem_q)) return rc;
-  if (int rc = set_smem(k_score_dkv_simt<T, D>, smem_k)) return rc;
-  k_score_dq_simt<T, D><<<dim3((a.Nq + BT - 1) / BT, a.H, a.B), kThreads, smem_q, s>>>(a);
-  k_score_dkv_simt<T, D><<<dim3((a.Nk + BT - 1) / BT, a.Hkv, a.B), kThreads, smem_k, s>>>(a);
+  if (int rc = set_smem(k_score_dq_simt<D>, smem_q)) return rc;
+  if (int rc = set_smem(k_score_dkv_simt<D>, smem_k)) return rc;
+  k_score_dq_simt<D><<<dim3((a.Nq + BT - 1) / BT, a.H, a.B), kThreads, smem_q, s>>>(a);
+  k_score_dkv_simt<D><<<dim3((a.Nk + BT - 1) / BT, a.Hkv, a.B), kThreads, smem_k, s>>>(a);
   count_launch(2);
   return check_launch("k_score_bwd_simt");
 }
 
 }  // namespace
 
-int launch_score_fwd_simt(const ScoreArgs& a, int d, int dtype, cudaStream_t s) {
-  if (dtype == CALIBATT_BF16) return d == 128 ? fwd<__nv_bfloat16, 128>(a, s) : fwd<__nv_bfloat16, 64>(a, s);
-  return d == 128 ? fwd<float, 128>(a, s) : fwd<float, 64>(a, s);
-}
-
-int launch_score_bwd_simt(const ScoreArgs& a, int d, int dtype, cudaStream_t s) {
-  if (dtype == CALIBATT_BF16) return d == 128 ? bwd<__nv_bfloat16, 128>(a, s) : bwd<__nv_bfloat16, 64>(a, s);
-  return d == 128 ? bwd<float, 128>(a, s) : bwd<float, 64>(a, s);
-}
+int launch_score_fwd_simt(const ScoreArgs& a, int d, cudaStream_t s) { return d == 128 ? fwd<128>(a, s) : fwd<64>(a, s); }
+int launch_score_bwd_simt(const ScoreArgs& a, int d, cudaStream_t s) { return d == 128 ? bwd<128>(a, s) : bwd<64>(a, s); }
 
 }  // namespace calibatt
