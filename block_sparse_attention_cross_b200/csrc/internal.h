@@ -100,8 +100,8 @@ struct ScoreArgs {
   int splits, packed;       // forward: splits of the key axis; packed: the G heads of a key head share a tile
   float* part_o;            // [B, H, Nq, splits, d]
   float* part_lse;          // [B, H, Nq, splits]
-  float* row_lse;           // backward: [B, H, 128 nqb], see score_rows.cu
-  float* row_d;             // backward: [B, H, 128 nqb]
+  float* row_lse;           // backward: [B, H, 128 nqb]; fp32: LSE, +inf where a row sees nothing; bf16: -log2(e) of it
+  float* row_d;             // backward: [B, H, 128 nqb]; fp32: D; bf16: -D
   int2* row_span;           // backward, bf16: [B, 128 nqb] the rows' intervals, padded to whole tiles
   float* part_table;        // backward: [B, H, table tiles, n_buckets]
   int table_tiles;          // query tiles per head that write part_table
@@ -121,8 +121,8 @@ int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_attn_spans(int B, int Nq, int Nk, int causal, const int32_t* docs, int n_docs, const int32_t* prefix,
                       const int32_t* kv_len, const int32_t* q_len, const int32_t* q_start, int2* row, int4* tile,
                       int32_t* q_start_out, cudaStream_t s);
-// score_rows.cu: per-row terms of the backward pass, the sum of the table's partial gradients
-int launch_score_rows(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
+// score_rows.cu: per-row terms of the fp32 backward pass, the sum of the table's partial gradients
+int launch_score_rows(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_score_table_sum(const ScoreArgs& a, int dtype, cudaStream_t s);
 
 // select_vote.cu

@@ -284,8 +284,9 @@ int calibatt_score_attn_bwd(const calibatt_tensor4* dout, const calibatt_tensor4
     return set_error(CALIBATT_E_WORKSPACE, "workspace of %zu bytes (256-byte aligned) needed, %zu given", need,
                      workspace_bytes);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if ((rc = launch_score_rows(a, d, dtype, s))) return rc;
-  if ((rc = dtype == CALIBATT_BF16 ? launch_score_bwd_tc(a, d, s) : launch_score_bwd_simt(a, d, s))) return rc;
+  if (dtype == CALIBATT_BF16) rc = launch_score_bwd_tc(a, d, s);
+  else if ((rc = launch_score_rows(a, d, s)) == CALIBATT_OK) rc = launch_score_bwd_simt(a, d, s);
+  if (rc) return rc;
   return dtable != nullptr ? launch_score_table_sum(a, dtype, s) : CALIBATT_OK;
 }
 

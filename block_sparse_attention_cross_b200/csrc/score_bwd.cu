@@ -3,18 +3,23 @@
 // Two kernels, each recomputing the scores, so that every gradient is summed
 // by one CTA in a fixed order, without atomics and without an fp32 buffer for
 // dQ:
-//   k_score_dkv  one 128-key tile of a key head: for every query tile that
+//   k_score_dq   one 128-query tile (TMEM lanes are queries), two sweeps over
+//                the key tiles that it sees.  The first forms S = Q K^T and
+//                dP = dO V^T and sums D = sum_j P dP of every row in fp32.  (D
+//                could be had as dO . O, but O is rounded to bf16, and that
+//                error, common to a whole row of dZ = P (dP - D), would double
+//                the error of dQ and of the table's gradient.)  The second
+//                forms S and dP again, then dQ += dS K and the sums of dZ by
+//                bucket.
+//   k_score_dkv  one 128-key tile of a key head (TMEM lanes are keys), after k_score_dq: for every query tile that
 //                sees it (all G query heads) S^T = K Q^T and dP^T = V dO^T,
-//                then dV += P^T dO and dK += dS^T Q.  TMEM lanes are keys.
-//   k_score_dq   one 128-query tile: for every key tile S = Q K^T and
-//                dP = dO V^T, then dQ += dS K; and the sums of dZ by bucket.
-//                TMEM lanes are queries.
+//                then dV += P^T dO and dK += dS^T Q.
 // Both products that read a probability or dS take it as the A operand from
 // TMEM, where the softmax warps leave it as bf16 in place of the scores; the
 // other operand is the input tile as it lies in shared memory (128-byte
 // swizzle, read K-major by the first products and MN-major by the second).
-// Seven 128 x 128 x d products a tile pair instead of the five that one kernel
-// with atomics on dQ would need.
+// Nine 128 x 128 x d products a tile pair (2 + 3 + 4) instead of the five of
+// one kernel with atomics on dQ and D from the rounded O.
 //
 // A CTA (one per SM): warps 0-3 and 4-7 softmax, the lanes' columns split in
 // halves of 64 between the warpgroups; warp 8 TMA producer; warp 9 MMA issuer;
@@ -524,13 +529,17 @@ struct DqLayout {
 template <int RK, int RV>
 struct DqCtrl {
   uint64_t q_full, k_full[RK], k_empty[RK], v_full[RV], v_empty[RV];
+  uint64_t a_full[2], a_free[2], mid;   // first sweep
   uint64_t s_full[2], dp_full, ds_full, o_full, drain;
   uint64_t win_full[2], win_empty[2];
   uint32_t tmem_base;
   int abort;
+  float d_part[2][TILE];   // the column halves' sums of P dP
 };
 
-// TMEM: S of key tile t in [128 (t & 1), + 128), dS in place; dP [256, 384);
+// First sweep: S and dP of key tile t in the column pairs [128 (t & 1), + 128)
+// and [256 + 128 (t & 1), + 128), issued two tiles ahead of the softmax warps.
+// Second sweep: S of key tile t in [128 (t & 1), + 128), dS in place; dP [256, 384);
 // dQ at 384.  Issue order: S(0), dP(0), S(1); then per tile t, once dS(t) is
 // stored, dP(t + 1), dQ(t), S(t + 2): the scores are a tile ahead, so the
 // exponentials of tile t + 1 start at once, and dP(t + 1) arrives during them.
@@ -565,10 +574,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c->v_empty[e], 1);
     }
     for (int e = 0; e < 2; ++e) {
+      mbar_init(&c->a_full[e], 1);
+      mbar_init(&c->a_free[e], 256);
       mbar_init(&c->s_full[e], 1);
       mbar_init(&c->win_full[e], 32);
       mbar_init(&c->win_empty[e], 256);
     }
+    mbar_init(&c->mid, 256);
     mbar_init(&c->dp_full, 1);
     mbar_init(&c->ds_full, 256);
     mbar_init(&c->o_full, 1);
@@ -598,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const bool any = key_start(a, h, qb, lo, hi, w);
     uint32_t t = 0;
+    int sweep = 0;
     bool loaded_v = true;   // the last tile's V copy was issued too
     const uint64_t pol = l2_policy_evict_last(), pol_q = l2_policy_evict_first();
     if (any) {
@@ -625,8 +638,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < D / 64; ++x)
         tma_load_4d_w(smem + L::OFF_V + v * L::TB + x * L::BOX, &tmV, x * 64, w.kb * TILE, hk, b, &c->v_full[v], pol);
       loaded_v = true;
-      if (w.next < 0) break;
-      key_next(a, h, qb, w);
+      if (w.next >= 0) key_next(a, h, qb, w);
+      else if (sweep++ == 0) key_start(a, h, qb, lo, hi, w);
+      else break;
     }
     if (lane == 0) {
       if (!ok) {
@@ -661,26 +675,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       return ok;
     };
-    auto sK = [&](uint32_t t) { return smem_u32(smem + L::OFF_K + (t % RK) * L::TB); };
+    // u: position in the rings, which go on from the first sweep to the second
+    auto sK = [&](uint32_t u) { return smem_u32(smem + L::OFF_K + (u % RK) * L::TB); };
+    auto qk = [&](uint32_t u, uint32_t dst) {
+      if (!wait(&c->k_full[u % RK], (u / RK) & 1)) return false;
+      mma_scores<D>(dst, sQ, sK(u), IDESC_S);
+      return true;
+    };
+    auto ov = [&](uint32_t u, uint32_t dst) {
+      if (!wait(&c->v_full[u % RV], (u / RV) & 1)) return false;
+      mma_scores<D>(dst, sO, smem_u32(smem + L::OFF_V + (u % RV) * L::TB), IDESC_S);
+      mma_commit_w(&c->v_empty[u % RV]);
+      return true;
+    };
     auto scores = [&](uint32_t t) {
-      if (!wait(&c->k_full[t % RK], (t / RK) & 1)) return false;
-      mma_scores<D>(tmem + (t & 1) * 128, sQ, sK(t), IDESC_S);
+      if (!qk(n + t, tmem + (t & 1) * 128)) return false;
       mma_commit_w(&c->s_full[t & 1]);
       return true;
     };
     auto grads = [&](uint32_t t) {
-      if (!wait(&c->v_full[t % RV], (t / RV) & 1)) return false;
-      mma_scores<D>(tP, sO, smem_u32(smem + L::OFF_V + (t % RV) * L::TB), IDESC_S);
+      if (!ov(n + t, tP)) return false;
       mma_commit_w(&c->dp_full);
-      mma_commit_w(&c->v_empty[t % RV]);
       return true;
     };
-    if (n > 0 && wait(&c->q_full, 0) && scores(0) && grads(0) && (n == 1 || scores(1))) {
+    if (n > 0 && wait(&c->q_full, 0)) {
+      for (uint32_t t = 0; t < n; ++t) {
+        if (!wait(&c->a_free[t & 1], ((t >> 1) & 1) ^ 1)) break;
+        if (!qk(t, tmem + (t & 1) * 128)) break;
+        mma_commit_w(&c->k_empty[t % RK]);
+        if (!ov(t, tP + (t & 1) * 128)) break;
+        mma_commit_w(&c->a_full[t & 1]);
+      }
+    }
+    if (n > 0 && ok && wait(&c->mid, 0) && scores(0) && grads(0) && (n == 1 || scores(1))) {
       for (uint32_t t = 0; t < n; ++t) {
         if (!wait(&c->ds_full, t & 1)) break;
         if (t + 1 < n && !grads(t + 1)) break;
-        mma_from_tmem(tQ, tmem + (t & 1) * 128, sK(t), IDESC_O, t > 0 ? 1u : 0u);
-        mma_commit_w(&c->k_empty[t % RK]);
+        mma_from_tmem(tQ, tmem + (t & 1) * 128, sK(n + t), IDESC_O, t > 0 ? 1u : 0u);
+        mma_commit_w(&c->k_empty[(n + t) % RK]);
         if (t + 1 == n) mma_commit_w(&c->o_full);
         if (t + 2 < n && !scores(t + 2)) break;
       }
@@ -697,6 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       KeyWalk w;
       bool bad = false, ok = true;
       uint32_t t = 0;
+      int sweep = 0;
       for (bool more = key_start(a, h, qb, lo, hi, w); more; ++t) {
         const int e = t & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(&c->win_empty[e], ((t >> 1) & 1) ^ 1, &c->abort, a.spin_ns));
@@ -705,8 +738,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           fill_window(a, h, w.kb * TILE, p0, reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256,
                       smem + L::OFF_BWIN + e * 256, &bad);
         mbar_arrive(&c->win_full[e]);
-        more = w.next >= 0;
-        if (more) key_next(a, h, qb, w);
+        if (w.next >= 0) key_next(a, h, qb, w);
+        else more = sweep++ == 0 && key_start(a, h, qb, lo, hi, w);
       }
       if (!ok) {
         c->abort = 1;
@@ -724,9 +757,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool xform = a.cap > 0.f || a.slopes != nullptr || a.table != nullptr;
     const uint64_t c2x2 = f2pack(xform ? 1.f : terms.sc, xform ? 1.f : terms.sc);
     const int2 vis = score_row(a, b, i);
-    const size_t r0 = (static_cast<size_t>(b) * a.H + h) * a.nqb * TILE + i;
-    const float nlse = a.row_lse[r0], nd = a.row_d[r0];
-    const uint64_t nlse2 = f2pack(nlse, nlse), nd2 = f2pack(nd, nd);
+    // -log2(e) LSE; -inf (P = 0) where the row sees nothing
+    float nlse = -INFINITY;
+    if (vis.x < vis.y) {
+      const float x = a.lse[(static_cast<size_t>(b) * a.H + h) * a.Nq + i];
+      if (x != -INFINITY) nlse = -kLog2e * x;
+    }
+    uint64_t nlse2 = f2pack(nlse, nlse);
     const float slope = a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
     float far_lo = 0.f, far_hi = 0.f, sum_lo = 0.f, sum_hi = 0.f;
     int n_lo = 0, n_hi = 0;
@@ -740,16 +777,90 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
     }
     bool ok = true;
-    uint32_t t = 0;
+    uint32_t t = 0, wt = 0;   // wt: windows consumed, over both sweeps
     KeyWalk w;
-    for (bool more = key_start(a, h, qb, lo, hi, w); more; ++t) {
+    // ---- first sweep: D = sum over the visible keys of P dP ------------------
+    float d_sum = 0.f;
+    for (bool more = key_start(a, h, qb, lo, hi, w); more; ++t, ++wt) {
       const int k0 = w.kb * TILE;
       const uint32_t tSh = tmem + (t & 1) * 128 + lanes + half * 64;
       const bool edge = k0 < tr.z || k0 + TILE > tr.w;
       const bool near = is_near(a, k0, p0);
+      bool got = mbar_wait(&c->a_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && a.table != nullptr) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
+      ok = __all_sync(0xffffffffu, got);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t r[64], g[64];
+      tmem_ld32(tSh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+      tmem_ld32(tSh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+      tmem_ld32(tSh + 256, *reinterpret_cast<uint32_t(*)[32]>(&g[0]));
+      tmem_ld32(tSh + 288, *reinterpret_cast<uint32_t(*)[32]>(&g[32]));
+      tmem_ld_wait();
+      reg_fence(r);
+      reg_fence(g);
+      tc_fence_before();
+      mbar_arrive(&c->a_free[t & 1]);
+      if (xform) {
+        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (wt & 1) * 256 + TILE - 1 - row + half * 64;
+        float none[64];
+        score_columns<1, false>(a, terms, r, none, slope, static_cast<float>(k0 + half * 64 - p0 - row), near, wr,
+                                k0 > p0 ? far_hi : far_lo);
+        if (a.table != nullptr) mbar_arrive(&c->win_empty[wt & 1]);
+      }
+      if (edge) {
+        const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;
+#pragma unroll
+        for (int x = 0; x < 64; ++x)
+          if (x < e0 || x >= e1) {
+            r[x] = f2u(-INFINITY);
+            g[x] = 0;
+          }
+      }
+      uint64_t s0 = f2pack(0.f, 0.f), s1 = s0;
+#pragma unroll
+      for (int x = 0; x < 64; x += 2) {
+        float y0, y1;
+        f2unpack(ffma2(f2pack(u2f(r[x]), u2f(r[x + 1])), c2x2, nlse2), y0, y1);
+        const uint64_t pp = f2pack(ex2_approx(y0), ex2_approx(y1)), gg = f2pack(u2f(g[x]), u2f(g[x + 1]));
+        if (x & 2) s1 = ffma2(pp, gg, s1); else s0 = ffma2(pp, gg, s0);
+      }
+      float u0, u1, v0, v1;
+      f2unpack(s0, u0, u1);
+      f2unpack(s1, v0, v1);
+      d_sum += (u0 + u1) + (v0 + v1);
+      more = w.next >= 0;
+      if (more) key_next(a, h, qb, w);
+    }
+    float nd = 0.f;
+    if (ok) {
+      c->d_part[half][row] = d_sum;
+      mbar_arrive(&c->mid);
+      ok = __all_sync(0xffffffffu, mbar_wait(&c->mid, 0, &c->abort, a.spin_ns));
+      nd = -(c->d_part[0][row] + c->d_part[1][row]);
+      // A row with a non-finite dO (or V that it sees) marks every gradient it
+      // enters: its probabilities become NaN.
+      if (!isfinite(nd)) nlse = NAN;
+      nlse2 = f2pack(nlse, nlse);
+      if (half == 0) {
+        const size_t r0 = (static_cast<size_t>(b) * a.H + h) * a.nqb * TILE + i;
+        a.row_lse[r0] = nlse;
+        a.row_d[r0] = nd;
+        if (h == 0) a.row_span[static_cast<size_t>(b) * a.nqb * TILE + i] = vis;
+      }
+    }
+    const uint64_t nd2 = f2pack(nd, nd);
+    // ---- second sweep ----------------------------------------------------------
+    t = 0;
+    for (bool more = ok && key_start(a, h, qb, lo, hi, w); more; ++t, ++wt) {
+      const int k0 = w.kb * TILE;
+      const uint32_t tSh = tmem + (t & 1) * 128 + lanes + half * 64;
+      const bool edge = k0 < tr.z || k0 + TILE > tr.w;
+      const bool near = is_near(a, k0, p0);
+      const uint32_t u = wt;   // position in the K ring
       bool got = mbar_wait(&c->s_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
-      if (got && a.table != nullptr) got = mbar_wait(&c->win_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
-      if (got && edge) got = mbar_wait(&c->k_full[t % RK], (t / RK) & 1, &c->abort, a.spin_ns);
+      if (got && a.table != nullptr) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && edge) got = mbar_wait(&c->k_full[u % RK], (u / RK) & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
@@ -760,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       reg_fence(r);
       float f[64];
       if (xform) {
-        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (t & 1) * 256 + TILE - 1 - row + half * 64;
+        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (wt & 1) * 256 + TILE - 1 - row + half * 64;
         score_columns<1, true>(a, terms, r, f, slope, static_cast<float>(k0 + half * 64 - p0 - row), near, wr,
                                k0 > p0 ? far_hi : far_lo);
       } else {
@@ -770,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (edge && half < D / 64) {
         // Keys with a NaN or an infinity: zeroed before dQ reads them (S, which
         // is complete, has made a visible one's dS NaN).
-        clean_box_row(smem + L::OFF_K + (t % RK) * L::TB + half * L::BOX + row * 128, row);
+        clean_box_row(smem + L::OFF_K + (u % RK) * L::TB + half * L::BOX + row * 128, row);
         fence_proxy_async_smem();
       }
       float p[64];
@@ -804,7 +915,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // diagonal that ends in it; 31 more steps drain the others.  Runs of
           // offsets of one bucket are added up before the warp's own
           // accumulators are touched, so the order is fixed.
-          const uint8_t* bw = smem + L::OFF_BWIN + (t & 1) * 256 + half * 64 + 96 - w4 * 32;
+          const uint8_t* bw = smem + L::OFF_BWIN + (wt & 1) * 256 + half * 64 + 96 - w4 * 32;
           float* acc = hist + warp * 256;
           float diag = 0.f, run = 0.f;
           int cur = bw[0];
@@ -841,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k0 > p0) sum_hi += s0 + s1; else sum_lo += s0 + s1;
         }
       }
-      if (a.table != nullptr) mbar_arrive(&c->win_empty[t & 1]);
+      if (a.table != nullptr) mbar_arrive(&c->win_empty[wt & 1]);
 #pragma unroll
       for (int x = 0; x < 64; ++x) p[x] *= f[x];
       store_half(tSh, p);
@@ -911,8 +1022,8 @@ int launch(const ScoreArgs& a, cudaStream_t s) {
     return rc;
   if ((rc = configure_kernel(reinterpret_cast<const void*>(dq), done_q, DqLayout<D>::SMEM, kLaunchRegs, "k_score_dq")))
     return rc;
-  dkv<<<static_cast<unsigned>(nk), kThreads, DkvLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
   dq<<<static_cast<unsigned>(nq), kThreads, DqLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
+  dkv<<<static_cast<unsigned>(nk), kThreads, DkvLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
   count_launch(2);
   return check_launch("k_score_bwd");
 }

@@ -5,13 +5,11 @@
 namespace calibatt {
 namespace {
 
-// D_i = sum over d of dO_i O_i, and the row's LSE as the backward kernels read
-// it: +inf where the row sees nothing (every probability becomes 0), NaN where
-// D is not finite (so that a row with a non-finite dO or O marks every
-// gradient it enters).  One warp a row: reads dO and O once, DRAM-bound.
-// The tensor-core kernels (bf16) add both terms to packed pairs: they get
-// -log2(e) LSE and -D, and the rows' intervals padded to whole tiles.
-template <typename T, int D>
+// fp32: D_i = sum over d of dO_i O_i, and the row's LSE as the backward
+// kernels read it: +inf where the row sees nothing (every probability becomes
+// 0), NaN where D is not finite (so that a row with a non-finite dO or O marks
+// every gradient it enters).  One warp a row: reads dO and O once, DRAM-bound.
+template <int D>
 __global__ void __launch_bounds__(256) k_score_rows(const ScoreArgs a) {
   const long long rows = 128ll * a.nqb;
   const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -22,19 +20,10 @@ __global__ void __launch_bounds__(256) k_score_rows(const ScoreArgs a) {
   float sum = 0.f, lse = INFINITY;
   const int2 r = score_row(a, b, i);
   if (r.x < r.y) {
-    const T* po = reinterpret_cast<const T*>(a.o.p) + b * a.o.sb + h * a.o.sh + i * a.o.sn;
-    const T* pd = reinterpret_cast<const T*>(a.dout.p) + b * a.dout.sb + h * a.dout.sh + i * a.dout.sn;
-    if constexpr (sizeof(T) == 2) {
+    const float* po = reinterpret_cast<const float*>(a.o.p) + b * a.o.sb + h * a.o.sh + i * a.o.sn;
+    const float* pd = reinterpret_cast<const float*>(a.dout.p) + b * a.dout.sb + h * a.dout.sh + i * a.dout.sn;
 #pragma unroll
-      for (int x = lane * 2; x < D; x += 64) {
-        const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(po + x));
-        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(pd + x));
-        sum = fmaf(u.x, v.x, fmaf(u.y, v.y, sum));
-      }
-    } else {
-#pragma unroll
-      for (int x = lane; x < D; x += 32) sum = fmaf(po[x], pd[x], sum);
-    }
+    for (int x = lane; x < D; x += 32) sum = fmaf(po[x], pd[x], sum);
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     lse = a.lse[static_cast<size_t>(bh) * a.Nq + i];
@@ -42,9 +31,8 @@ __global__ void __launch_bounds__(256) k_score_rows(const ScoreArgs a) {
     else if (!isfinite(sum)) lse = NAN;
   }
   if (lane == 0) {
-    a.row_lse[w] = sizeof(T) == 2 ? -kLog2e * lse : lse;
-    a.row_d[w] = sizeof(T) == 2 ? -sum : sum;
-    if (sizeof(T) == 2 && h == 0) a.row_span[b * rows + i] = r;
+    a.row_lse[w] = lse;
+    a.row_d[w] = sum;
   }
 }
 
@@ -76,16 +64,11 @@ __global__ void __launch_bounds__(128) k_score_table_sum(const ScoreArgs a) {
 
 }  // namespace
 
-int launch_score_rows(const ScoreArgs& a, int d, int dtype, cudaStream_t s) {
+int launch_score_rows(const ScoreArgs& a, int d, cudaStream_t s) {
   const long long rows = 128ll * a.nqb * a.B * a.H;
   const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-  if (dtype == CALIBATT_BF16) {
-    if (d == 128) k_score_rows<__nv_bfloat16, 128><<<grid, 256, 0, s>>>(a);
-    else k_score_rows<__nv_bfloat16, 64><<<grid, 256, 0, s>>>(a);
-  } else {
-    if (d == 128) k_score_rows<float, 128><<<grid, 256, 0, s>>>(a);
-    else k_score_rows<float, 64><<<grid, 256, 0, s>>>(a);
-  }
+  if (d == 128) k_score_rows<128><<<grid, 256, 0, s>>>(a);
+  else k_score_rows<64><<<grid, 256, 0, s>>>(a);
   count_launch();
   return check_launch("k_score_rows");
 }
