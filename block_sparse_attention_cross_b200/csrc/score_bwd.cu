@@ -41,6 +41,7 @@ constexpr uint32_t kControlRegs = 88;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
 constexpr int kProducer = 8, kMma = 9, kWindow = 10;
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kCtrlBytes = 2048;              // barriers and small state, checked against its size below
 constexpr uint32_t kRowBytes = 512 + 512 + 1024;   // -LSE, -D and interval of a tile's rows
 
 template <int D>
@@ -63,25 +64,6 @@ __device__ __forceinline__ void mma_from_tmem(uint32_t t, uint32_t ta, uint32_t 
   mma_ts_k64_w(t, ta + 64, bd + 512, idesc, 1u);
 }
 
-// Whether the table's value varies over a tile pair: some offset is nearer than the distance on its side.
-__device__ __forceinline__ bool is_near(const ScoreArgs& a, int k0, int p0) {
-  return a.table != nullptr && k0 - (p0 + TILE - 1) < a.R && k0 + TILE - 1 - p0 > -a.R;
-}
-
-// Warp 10's work for one tile pair: the table's values (and buckets) of the
-// offsets k0 - p0 - 127 ... k0 - p0 + 127.
-__device__ __forceinline__ void fill_window(const ScoreArgs& a, int h, int k0, int p0, float* win, uint8_t* bwin, bool* bad) {
-  const __nv_bfloat16* tab = reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
-  int n[8];
-#pragma unroll
-  for (int x = 0; x < 8; ++x) n[x] = score_bucket(a, k0 - p0 - (TILE - 1) + x * 32 + lane_id(), bad);
-#pragma unroll
-  for (int x = 0; x < 8; ++x) {
-    win[x * 32 + lane_id()] = __bfloat162float(tab[n[x]]) * kLog2e;
-    if (bwin != nullptr) bwin[x * 32 + lane_id()] = static_cast<uint8_t>(n[x]);
-  }
-}
-
 // ===========================================================================
 // dK, dV
 // ===========================================================================
@@ -98,7 +80,7 @@ struct DkvLayout {
   static constexpr uint32_t OFF_ROWS = OFF_DO + RING * TB;
   static constexpr uint32_t OFF_WIN = OFF_ROWS + RING * kRowBytes;   // float [2][256]
   static constexpr uint32_t OFF_CTRL = OFF_WIN + 2048;
-  static constexpr uint32_t SMEM = OFF_CTRL + 1024 + 1024;
+  static constexpr uint32_t SMEM = OFF_CTRL + kCtrlBytes + 1024;   // + alignment slack
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -107,6 +89,7 @@ struct DkvCtrl {
   uint64_t kv_full, ring_full[RING], ring_empty[RING];
   uint64_t s_full, p_full, dp_full, ds_full, o_full, drain;
   uint64_t win_full[2], win_empty[2];
+  WindowInfo win_info[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -194,13 +177,14 @@ __device__ __forceinline__ void zero_row(__nv_bfloat16* dst, bool live) {
 // stored, dV(t) and S(t + 1), and once dS(t) is stored, dK(t) and dP(t + 1):
 // the exponentials of pair t + 1 run while dK(t) and dP(t + 1) do, the
 // products' second half of the softmax (dS) while dV and S of the next do.
-template <int D>
+template <int D, int F>
 __global__ void __launch_bounds__(kThreads, 1)
     k_score_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                 const __grid_constant__ ScoreArgs a) {
   using L = DkvLayout<D>;
   constexpr int R = L::RING;
+  static_assert(sizeof(DkvCtrl<R>) <= kCtrlBytes, "control block");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   DkvCtrl<R>* c = reinterpret_cast<DkvCtrl<R>*>(smem + L::OFF_CTRL);
@@ -337,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_w(&c->drain);
     mbar_wait(&c->drain, 0, nullptr, a.spin_ns);
   } else if (warp == kWindow) {
-    if (a.table != nullptr) {
+    if (((F & kBias) && a.table != nullptr)) {
       QueryWalk w;
       bool bad = false, ok = true;
       uint32_t t = 0;
@@ -346,8 +330,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(&c->win_empty[e], ((t >> 1) & 1) ^ 1, &c->abort, a.spin_ns));
         if (!ok) break;
         const int p0 = a.q_start[b] + w.qb * TILE;
-        if (is_near(a, k0, p0))
-          fill_window(a, hk * a.G + w.g, k0, p0, reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256, nullptr, &bad);
+        if (is_near(a, k0, p0, p0 + TILE - 1))
+          fill_window(a, hk * a.G + w.g, 1, k0 - p0 - (TILE - 1), reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256, nullptr,
+                      &c->win_info[e], &bad);
         mbar_arrive(&c->win_full[e]);
       }
       if (!ok) {
@@ -362,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
     const uint32_t tSh = tS + lanes + half * 64, tPh = tP + lanes + half * 64;
     const ScoreTerms terms = score_terms(a);
-    const bool xform = a.cap > 0.f || a.slopes != nullptr || a.table != nullptr;
+    constexpr bool xform = F != 0;
     const uint64_t c2x2 = f2pack(xform ? 1.f : terms.sc, xform ? 1.f : terms.sc);
     const int j = k0 + row;
     bool ok = true;
@@ -373,13 +358,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p0 = a.q_start[b] + w.qb * TILE;
       const int4 tr = score_tile(a, b, w.qb);
       const bool edge = k0 < tr.z || k0 + TILE > tr.w;
-      const bool near = is_near(a, k0, p0);
+      const bool near = (F & kBias) && is_near(a, k0, p0, p0 + TILE - 1);
       const uint8_t* rows = smem + L::OFF_ROWS + e * kRowBytes;
       const float4* nlse = reinterpret_cast<const float4*>(rows) + half * 16;
       const float4* nd = reinterpret_cast<const float4*>(rows + 512) + half * 16;
       float slope = 0.f, far = 0.f;
-      if (a.slopes != nullptr) slope = a.slopes[h] * kLog2e;
-      if (a.table != nullptr && !near) {
+      if (((F & kBias) && a.slopes != nullptr)) slope = a.slopes[h] * kLog2e;
+      if (((F & kBias) && a.table != nullptr) && !near) {
         bool bad = false;
         const int n = score_bucket(a, k0 > p0 ? a.R : -a.R, &bad);
         far = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n]) * kLog2e;
@@ -387,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bool got = mbar_wait(&c->s_full, t & 1, &c->abort, a.spin_ns) &&
                  mbar_wait(&c->ring_full[e], (t / R) & 1, &c->abort, a.spin_ns);
-      if (got && a.table != nullptr) got = mbar_wait(&c->win_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && ((F & kBias) && a.table != nullptr)) got = mbar_wait(&c->win_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
       if (got && edge) got = mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
@@ -397,16 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(tSh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
       tmem_ld_wait();
       reg_fence(r);
-      float pf[64];   // first the cap's factor, then P times it
-      if (xform) {
-        // column x: query 64 half + x, offset j - p falls with x
-        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (t & 1) * 256 + row + TILE - 1 - half * 64;
-        score_columns<-1, true>(a, terms, r, pf, slope, static_cast<float>(j - p0 - half * 64), near, wr, far);
-        if (a.table != nullptr) mbar_arrive(&c->win_empty[t & 1]);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 64; ++x) pf[x] = 1.f;
-      }
       uint32_t seen0 = 0xffffffffu, seen1 = 0xffffffffu;
       if (edge) {
         const int4* span = reinterpret_cast<const int4*>(rows + 1024) + half * 32;
@@ -417,6 +392,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bits = (j >= v.x && j < v.y ? 1u : 0u) | (j >= v.z && j < v.w ? 2u : 0u);
           if (x < 32) seen0 |= bits << x; else seen1 |= bits << (x - 32);
         }
+      }
+      float pf[64];   // first the cap's factor, then P times it
+      if (xform) {
+        // column x: query 64 half + x, offset j - p falls with x
+        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (t & 1) * 256 + row + TILE - 1 - half * 64;
+        const bool window = near && c->win_info[t & 1].cuts > 0;
+        score_columns<F, -1, true>(a, terms, r, pf, slope, static_cast<float>(j - p0 - half * 64),
+                                k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
+                                near ? (window ? 0.f : wr[0]) : far, edge);
+        if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[t & 1]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 64; ++x) pf[x] = 1.f;
+      }
+      if (edge) {
         // Queries with a NaN or an infinity would leave it in every key's sums
         // through a probability of 0: their rows of Q (read by S, which is
         // complete) and of dO (read by dP, awaited above) are zeroed before
@@ -522,7 +512,7 @@ struct DqLayout {
   static constexpr uint32_t OFF_BWIN = OFF_WIN + 2048;      // uint8 [2][256]
   static constexpr uint32_t OFF_HIST = OFF_BWIN + 512;      // float [8 warps][256]
   static constexpr uint32_t OFF_CTRL = OFF_HIST + 8192;
-  static constexpr uint32_t SMEM = OFF_CTRL + 1024 + 1024;
+  static constexpr uint32_t SMEM = OFF_CTRL + kCtrlBytes + 1024;   // + alignment slack
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -532,6 +522,7 @@ struct DqCtrl {
   uint64_t a_full[2], a_free[2], mid;   // first sweep
   uint64_t s_full[2], dp_full, ds_full, o_full, drain;
   uint64_t win_full[2], win_empty[2];
+  WindowInfo win_info[2];
   uint32_t tmem_base;
   int abort;
   float d_part[2][TILE];   // the column halves' sums of P dP
@@ -543,13 +534,14 @@ struct DqCtrl {
 // dQ at 384.  Issue order: S(0), dP(0), S(1); then per tile t, once dS(t) is
 // stored, dP(t + 1), dQ(t), S(t + 2): the scores are a tile ahead, so the
 // exponentials of tile t + 1 start at once, and dP(t + 1) arrives during them.
-template <int D>
+template <int D, int F>
 __global__ void __launch_bounds__(kThreads, 1)
     k_score_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                const __grid_constant__ ScoreArgs a) {
   using L = DqLayout<D>;
   constexpr int RK = L::RK, RV = L::RV;
+  static_assert(sizeof(DqCtrl<RK, RV>) <= kCtrlBytes, "control block");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   DqCtrl<RK, RV>* c = reinterpret_cast<DqCtrl<RK, RV>*>(smem + L::OFF_CTRL);
@@ -592,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmDO);
   }
-  if (a.dtable != nullptr)
+  if (((F & kBias) && a.dtable != nullptr))
     for (int x = threadIdx.x; x < 8 * 256; x += kThreads) hist[x] = 0.f;
   if (warp == kMma) {
     tmem_alloc(&c->tmem_base, kTmemCols);
@@ -725,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_w(&c->drain);
     mbar_wait(&c->drain, 0, nullptr, a.spin_ns);
   } else if (warp == kWindow) {
-    if (a.table != nullptr) {
+    if (((F & kBias) && a.table != nullptr)) {
       KeyWalk w;
       bool bad = false, ok = true;
       uint32_t t = 0;
@@ -734,9 +726,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = t & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(&c->win_empty[e], ((t >> 1) & 1) ^ 1, &c->abort, a.spin_ns));
         if (!ok) break;
-        if (is_near(a, w.kb * TILE, p0))
-          fill_window(a, h, w.kb * TILE, p0, reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256,
-                      smem + L::OFF_BWIN + e * 256, &bad);
+        if (is_near(a, w.kb * TILE, p0, p0 + TILE - 1))
+          fill_window(a, h, 1, w.kb * TILE - p0 - (TILE - 1), reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256,
+                      smem + L::OFF_BWIN + e * 256, &c->win_info[e], &bad);
         mbar_arrive(&c->win_full[e]);
         if (w.next >= 0) key_next(a, h, qb, w);
         else more = sweep++ == 0 && key_start(a, h, qb, lo, hi, w);
@@ -754,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(w4 * 32) << 16;
     const uint32_t tPh = tP + lanes + half * 64;
     const ScoreTerms terms = score_terms(a);
-    const bool xform = a.cap > 0.f || a.slopes != nullptr || a.table != nullptr;
+    constexpr bool xform = F != 0;
     const uint64_t c2x2 = f2pack(xform ? 1.f : terms.sc, xform ? 1.f : terms.sc);
     const int2 vis = score_row(a, b, i);
     // -log2(e) LSE; -inf (P = 0) where the row sees nothing
@@ -764,10 +756,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x != -INFINITY) nlse = -kLog2e * x;
     }
     uint64_t nlse2 = f2pack(nlse, nlse);
-    const float slope = a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
+    const float slope = ((F & kBias) && a.slopes != nullptr) ? a.slopes[h] * kLog2e : 0.f;
     float far_lo = 0.f, far_hi = 0.f, sum_lo = 0.f, sum_hi = 0.f;
     int n_lo = 0, n_hi = 0;
-    if (a.table != nullptr) {
+    if (((F & kBias) && a.table != nullptr)) {
       bool bad = false;
       const __nv_bfloat16* tab = reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
       n_lo = score_bucket(a, -a.R, &bad);
@@ -785,9 +777,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int k0 = w.kb * TILE;
       const uint32_t tSh = tmem + (t & 1) * 128 + lanes + half * 64;
       const bool edge = k0 < tr.z || k0 + TILE > tr.w;
-      const bool near = is_near(a, k0, p0);
+      const bool near = (F & kBias) && is_near(a, k0, p0, p0 + TILE - 1);
       bool got = mbar_wait(&c->a_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
-      if (got && a.table != nullptr) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && ((F & kBias) && a.table != nullptr)) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
@@ -801,15 +793,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       reg_fence(g);
       tc_fence_before();
       mbar_arrive(&c->a_free[t & 1]);
+      const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;   // columns of the row's interval
       if (xform) {
         const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (wt & 1) * 256 + TILE - 1 - row + half * 64;
+        const bool window = near && c->win_info[wt & 1].cuts > 0;
         float none[64];
-        score_columns<1, false>(a, terms, r, none, slope, static_cast<float>(k0 + half * 64 - p0 - row), near, wr,
-                                k0 > p0 ? far_hi : far_lo);
-        if (a.table != nullptr) mbar_arrive(&c->win_empty[wt & 1]);
+        score_columns<F, 1, false>(a, terms, r, none, slope, static_cast<float>(k0 + half * 64 - p0 - row),
+                                k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
+                                near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo, edge);
+        if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[wt & 1]);
       }
       if (edge) {
-        const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;
 #pragma unroll
         for (int x = 0; x < 64; ++x)
           if (x < e0 || x >= e1) {
@@ -856,10 +850,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int k0 = w.kb * TILE;
       const uint32_t tSh = tmem + (t & 1) * 128 + lanes + half * 64;
       const bool edge = k0 < tr.z || k0 + TILE > tr.w;
-      const bool near = is_near(a, k0, p0);
+      const bool near = (F & kBias) && is_near(a, k0, p0, p0 + TILE - 1);
       const uint32_t u = wt;   // position in the K ring
       bool got = mbar_wait(&c->s_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
-      if (got && a.table != nullptr) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && ((F & kBias) && a.table != nullptr)) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
       if (got && edge) got = mbar_wait(&c->k_full[u % RK], (u / RK) & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
@@ -870,10 +864,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld_wait();
       reg_fence(r);
       float f[64];
+      const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;   // columns of the row's interval
       if (xform) {
         const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (wt & 1) * 256 + TILE - 1 - row + half * 64;
-        score_columns<1, true>(a, terms, r, f, slope, static_cast<float>(k0 + half * 64 - p0 - row), near, wr,
-                               k0 > p0 ? far_hi : far_lo);
+        const bool window = near && c->win_info[wt & 1].cuts > 0;
+        score_columns<F, 1, true>(a, terms, r, f, slope, static_cast<float>(k0 + half * 64 - p0 - row),
+                                k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
+                                near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo, edge);
       } else {
 #pragma unroll
         for (int x = 0; x < 64; ++x) f[x] = 1.f;
@@ -903,13 +900,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < 64; x += 2)
         f2unpack(fmul2(fadd2(f2pack(u2f(r[x]), u2f(r[x + 1])), nd2), f2pack(p[x], p[x + 1])), p[x], p[x + 1]);
       if (edge) {
-        const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;
 #pragma unroll
         for (int x = 0; x < 64; ++x)
           if (x < e0 || x >= e1) p[x] = f[x] = 0.f;   // the factor of a masked score may be NaN
       }
-      if (a.dtable != nullptr) {   // p is dZ
-        if (near) {
+      if (((F & kBias) && a.dtable != nullptr)) {   // p is dZ
+        const WindowInfo& info = c->win_info[wt & 1];
+        if (near && info.cuts <= kMaxCuts) {
+          // Few buckets in the tile pair's offsets: the row's sums up to each
+          // boundary (column x is entry 127 - row + 64 half + x), their
+          // differences added up over the warp in a fixed order.
+          float below[kMaxCuts + 1];
+#pragma unroll
+          for (int k = 0; k < kMaxCuts; ++k) {
+            if (k >= info.cuts) { below[k] = 0.f; continue; }
+            const int cut = info.at[k] - (TILE - 1 - row + half * 64);
+            float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+            for (int x = 0; x < 64; x += 2) {
+              if (x < cut) s0 += p[x];
+              if (x + 1 < cut) s1 += p[x + 1];
+            }
+            below[k] = s0 + s1;
+          }
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int x = 0; x < 64; x += 2) {
+            s0 += p[x];
+            s1 += p[x + 1];
+          }
+          below[kMaxCuts] = s0 + s1;
+          float before = 0.f;
+#pragma unroll
+          for (int k = 0; k <= kMaxCuts; ++k) {
+            if (k > info.cuts) break;
+            const float upto = k == info.cuts ? below[kMaxCuts] : below[k < kMaxCuts ? k : 0];
+            float v = upto - before;
+            before = upto;
+#pragma unroll
+            for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+            if (lane == 31) hist[warp * 256 + info.bucket[k]] += v;
+          }
+        } else if (near) {
           // Sums along the diagonals (one offset each) by passing a running
           // sum from row to row: after column x lane 31 holds the sum of the
           // diagonal that ends in it; 31 more steps drain the others.  Runs of
@@ -952,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (k0 > p0) sum_hi += s0 + s1; else sum_lo += s0 + s1;
         }
       }
-      if (a.table != nullptr) mbar_arrive(&c->win_empty[wt & 1]);
+      if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[wt & 1]);
 #pragma unroll
       for (int x = 0; x < 64; ++x) p[x] *= f[x];
       store_half(tSh, p);
@@ -977,7 +1009,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       c->abort = 1;
       report_status(a.status, CALIBATT_E_TIMEOUT);
     }
-    if (a.dtable != nullptr) {
+    if (((F & kBias) && a.dtable != nullptr)) {
 #pragma unroll
       for (int m = 16; m > 0; m >>= 1) {
         sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, m);
@@ -993,7 +1025,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (a.dtable != nullptr) {
+  if (((F & kBias) && a.dtable != nullptr)) {
     float* dst = a.part_table + ((static_cast<size_t>(b) * a.H + h) * a.table_tiles + qb) * a.n_buckets;
     for (int n = threadIdx.x; n < a.n_buckets; n += kThreads) {
       float s = 0.f;
@@ -1005,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
 }
 
-template <int D>
+template <int D, int F>
 int launch(const ScoreArgs& a, cudaStream_t s) {
   CUtensorMap tq, tk, tv, to;
   int rc;
@@ -1016,8 +1048,8 @@ int launch(const ScoreArgs& a, cudaStream_t s) {
   const long long nk = static_cast<long long>(a.B) * a.Hkv * a.nkb, nq = static_cast<long long>(a.B) * a.H * a.nqb;
   if (nk >= (1ll << 31) || nq >= (1ll << 31)) return set_error(CALIBATT_E_UNSUPPORTED, "too many tiles");
   static std::atomic<bool> done_kv[kMaxDevices], done_q[kMaxDevices];
-  auto dkv = k_score_dkv<D>;
-  auto dq = k_score_dq<D>;
+  auto dkv = k_score_dkv<D, F>;
+  auto dq = k_score_dq<D, F>;
   if ((rc = configure_kernel(reinterpret_cast<const void*>(dkv), done_kv, DkvLayout<D>::SMEM, kLaunchRegs, "k_score_dkv")))
     return rc;
   if ((rc = configure_kernel(reinterpret_cast<const void*>(dq), done_q, DqLayout<D>::SMEM, kLaunchRegs, "k_score_dq")))
@@ -1030,6 +1062,13 @@ int launch(const ScoreArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int launch_score_bwd_tc(const ScoreArgs& a, int d, cudaStream_t s) { return d == 128 ? launch<128>(a, s) : launch<64>(a, s); }
+int launch_score_bwd_tc(const ScoreArgs& a, int d, cudaStream_t s) {
+  switch ((a.cap > 0.f ? kCap : 0) | (a.slopes != nullptr || a.table != nullptr ? kBias : 0)) {
+    case 0: return d == 128 ? launch<128, 0>(a, s) : launch<64, 0>(a, s);
+    case kCap: return d == 128 ? launch<128, kCap>(a, s) : launch<64, kCap>(a, s);
+    case kBias: return d == 128 ? launch<128, kBias>(a, s) : launch<64, kBias>(a, s);
+    default: return d == 128 ? launch<128, kCap | kBias>(a, s) : launch<64, kCap | kBias>(a, s);
+  }
+}
 
 }  // namespace calibatt

@@ -63,6 +63,19 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   return d;
 }
 
+// Non-suspending test of a barrier's phase, for a warp that serves several.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Warp-collective: one elected lane issues the copy.
 __device__ __forceinline__ void tma_load_4d_w(void* dst, const CUtensorMap* tm, int x, int n, int h, int b, uint64_t* bar,
                                               uint64_t policy) {
@@ -146,49 +159,174 @@ __device__ __forceinline__ bool key_start(const ScoreArgs& a, int h, int qb, int
   return true;
 }
 
-// The score function on N columns of one thread's row, in log2 units.  DIR =
-// 1: the columns are keys, off0 the first one's offset j - p; DIR = -1: the
-// columns are queries.  `near`: the table's values for the columns are wr[DIR
-// x]; otherwise `far` is added.  With FACTOR, f becomes d c / d s of the cap.
-// cap tanh(x) = cap - 2 cap / (1 + e^(2x)) is right at both ends, and the
-// MUFU's relative errors stay 1e-7 of the cap.
+// ---- the table's values along the offsets of a tile pair ---------------------
+// A tile pair meets 255 offsets; entry x of a window is offset o0 + x.  Far
+// from zero a logarithmic bucket spans many offsets, so a window often holds
+// few buckets: up to four boundaries are listed, and a window of one bucket
+// needs no reads at all.
+constexpr int kMaxCuts = 4;
+struct WindowInfo {
+  int cuts;                  // boundaries; kMaxCuts + 1: more, see the per-offset arrays
+  int at[kMaxCuts];          // first entry of the next bucket
+  int bucket[kMaxCuts + 1];
+  int pad[2];
+};
+
+// Whether the table's value may vary over a tile of keys [k0, k0 + 128) and
+// rows at positions p0 ... p1: some offset is nearer than the distance.
+__device__ __forceinline__ bool is_near(const ScoreArgs& a, int k0, int p0, int p1) {
+  return a.table != nullptr && k0 - p1 < a.R && k0 + 127 - p0 > -a.R;
+}
+
+// Warp-collective; `heads` windows of consecutive heads from h0 on, 256 floats apart (log2 units).
+__device__ __forceinline__ void fill_window(const ScoreArgs& a, int h0, int heads, int o0, float* win, uint8_t* bwin,
+                                            WindowInfo* info, bool* bad) {
+  const int lane = lane_id();
+  int n[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) n[x] = score_bucket(a, o0 + x * 32 + lane, bad);
+  int cuts = 0;
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    int prev = __shfl_up_sync(0xffffffffu, n[x], 1);
+    const int last = __shfl_sync(0xffffffffu, n[x > 0 ? x - 1 : 0], 31);
+    if (lane == 0) prev = x > 0 ? last : n[0];
+    const bool cut = n[x] != prev && x * 32 + lane < 255;
+    const uint32_t m = __ballot_sync(0xffffffffu, cut);
+    const int at = cuts + __popc(m & ((1u << lane) - 1u));
+    if (cut && at < kMaxCuts) {
+      info->at[at] = x * 32 + lane;
+      info->bucket[at + 1] = n[x];
+    }
+    cuts += __popc(m);
+  }
+  if (lane == 0) {
+    info->cuts = min(cuts, kMaxCuts + 1);
+    info->bucket[0] = n[0];
+  }
+  for (int g = 0; g < heads; ++g) {
+    const __nv_bfloat16* tab =
+        reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h0 + g) * a.n_buckets;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) win[g * 256 + x * 32 + lane] = __bfloat162float(tab[n[x]]) * kLog2e;
+  }
+  if (bwin != nullptr) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) bwin[x * 32 + lane] = static_cast<uint8_t>(n[x]);
+  }
+}
+
+// ---- the score function on the columns of a thread's row ---------------------
+// In log2 units.  cap tanh(s scale / cap): where every |s scale / cap| of the
+// thread's columns is at most 0.6, an odd polynomial on the FMA pipe;
+// elsewhere cap - 2 cap / (1 + e^(2x)), two MUFU operations a score, right at
+// both ends.  Both stay within 3e-7 of the cap.  The polynomial leaves the
+// MUFU, which bounds the softmax, to the exponentials.  A row chooses by its
+// own scores, and in a tile that the mask cuts (`exact`) always takes the
+// second form, so no other row and no masked place changes a bit of it.
 struct ScoreTerms {
-  float sc, capA, kcap;   // scale log2e; cap log2e; 2 log2e scale / cap
+  float sc;                  // scale log2e
+  float capA, kcap, small;   // cap log2e; 2 log2e scale / cap; largest |s| for the polynomial
+  float inv;                 // 1 / (cap log2e)
+  float c[5];                // capped score = s (c0 + c1 s^2 + ... + c4 s^8)
 };
 __device__ __forceinline__ ScoreTerms score_terms(const ScoreArgs& a) {
-  ScoreTerms t;
+  ScoreTerms t = {};
   t.sc = a.scale * kLog2e;
-  t.capA = a.cap * kLog2e;
-  t.kcap = a.cap > 0.f ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+  if (a.cap > 0.f) {
+    const float k = a.scale / a.cap, k2 = k * k;
+    t.capA = a.cap * kLog2e;
+    t.kcap = 2.f * kLog2e * k;
+    t.small = 0.6f / k;
+    t.inv = 1.f / t.capA;
+    // tanh(x) / x as a polynomial in x^2, interpolated at the five Chebyshev
+    // nodes of [0, 0.36] (relative error at most 8e-8)
+    t.c[0] = 0.999999926f * t.sc;
+    t.c[1] = -0.333323020f * t.sc * k2;
+    t.c[2] = 0.133100644f * t.sc * k2 * k2;
+    t.c[3] = -0.052096653f * t.sc * k2 * k2 * k2;
+    t.c[4] = 0.015468751f * t.sc * k2 * k2 * k2 * k2;
+  }
   return t;
 }
-template <int DIR, bool FACTOR, int N>
+
+__device__ __forceinline__ uint64_t pair_of(const uint32_t* r, int x) { return f2pack(u2f(r[x]), u2f(r[x + 1])); }
+__device__ __forceinline__ void set_pair(uint32_t* r, int x, uint64_t v) {
+  float lo, hi;
+  f2unpack(v, lo, hi);
+  r[x] = f2u(lo);
+  r[x + 1] = f2u(hi);
+}
+
+// DIR = 1: the columns are keys, off0 the first one's offset j - p; DIR = -1:
+// the columns are queries.  side: +1 / -1 where every offset of the tile is >=
+// 0 / <= 0 (the distance is linear then), 0 otherwise.  window: the table's
+// value of column x is wr[DIR x], otherwise `flat` is added.  With FACTOR, f
+// becomes the derivative of the cap.
+// F: which terms the kernel was built for.  A kernel carries the code of its
+// own terms only: code that a call skips costs instruction-cache misses (all
+// terms in one kernel ran plain far tiles of a table at half the speed).
+enum ScoreForm { kCap = 1, kBias = 2 };
+template <int F, int DIR, bool FACTOR, int N>
 __device__ __forceinline__ void score_columns(const ScoreArgs& a, const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N],
-                                              float slope, float off0, bool near, const float* wr, float far) {
-  if (a.cap > 0.f) {
+                                              float slope, float off0, int side, bool window, const float* wr,
+                                              float flat, bool exact) {
+  // The constant part of the biases: the flat table value, and the distance
+  // of column 0 where the distance is linear over the tile.
+  const bool linear = (F & kBias) && a.slopes != nullptr && side != 0;
+  const float sl = side > 0 ? -slope : slope;   // -slope |off0 + DIR x| = sl (off0 + DIR x)
+  const float shift = F & kBias ? (window ? 0.f : flat) + (linear ? sl * off0 : 0.f) : 0.f;
+  const uint64_t shift2 = f2pack(shift, shift);
+  if (F & kCap) {
+    float big = 0.f, big1 = 0.f;
 #pragma unroll
-    for (int x = 0; x < N; ++x) {
-      const float rc = rcp_approx(1.f + ex2_approx(u2f(r[x]) * t.kcap));
-      if (FACTOR) f[x] = 4.f * (rc - rc * rc);
-      r[x] = f2u(fmaf(-2.f * t.capA, rc, t.capA));
+    for (int x = 0; x < N; x += 4) {
+      big = fmax3(big, fabsf(u2f(r[x])), fabsf(u2f(r[x + 1])));
+      big1 = fmax3(big1, fabsf(u2f(r[x + 2])), fabsf(u2f(r[x + 3])));
+    }
+    // (a NaN is not seen by the maximum; both forms pass it on)
+    if (!exact && fmaxf(big, big1) <= t.small) {
+      const uint64_t c0 = f2pack(t.c[0], t.c[0]), c1 = f2pack(t.c[1], t.c[1]), c2 = f2pack(t.c[2], t.c[2]),
+                     c3 = f2pack(t.c[3], t.c[3]), c4 = f2pack(t.c[4], t.c[4]);
+      const uint64_t iv = f2pack(t.inv, t.inv), one = f2pack(1.f, 1.f), neg = f2pack(-1.f, -1.f);
+#pragma unroll
+      for (int x = 0; x < N; x += 2) {
+        const uint64_t s = pair_of(r, x), v = fmul2(s, s);
+        const uint64_t q = ffma2(ffma2(ffma2(ffma2(c4, v, c3), v, c2), v, c1), v, c0);
+        set_pair(r, x, ffma2(s, q, shift2));
+        if (FACTOR) {
+          const uint64_t th = fmul2(fmul2(s, q), iv);
+          f2unpack(ffma2(fmul2(th, neg), th, one), f[x], f[x + 1]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < N; ++x) {
+        const float rc = rcp_approx(1.f + ex2_approx(u2f(r[x]) * t.kcap));
+        if (FACTOR) f[x] = 4.f * (rc - rc * rc);
+        r[x] = f2u(fmaf(-2.f * t.capA, rc, t.capA) + shift);
+      }
     }
   } else {
+    const uint64_t sc = f2pack(t.sc, t.sc);
 #pragma unroll
-    for (int x = 0; x < N; ++x) {
-      r[x] = f2u(u2f(r[x]) * t.sc);
-      if (FACTOR) f[x] = 1.f;
+    for (int x = 0; x < N; x += 2) set_pair(r, x, ffma2(pair_of(r, x), sc, shift2));
+    if (FACTOR) {
+#pragma unroll
+      for (int x = 0; x < N; ++x) f[x] = 1.f;
     }
   }
-  if (a.slopes != nullptr) {
+  if (!(F & kBias)) return;
+  if (linear) {
+#pragma unroll
+    for (int x = 0; x < N; ++x) r[x] = f2u(fmaf(sl, static_cast<float>(DIR * x), u2f(r[x])));
+  } else if (a.slopes != nullptr) {
 #pragma unroll
     for (int x = 0; x < N; ++x) r[x] = f2u(fmaf(-slope, fabsf(off0 + static_cast<float>(DIR * x)), u2f(r[x])));
   }
-  if (near) {
+  if (window) {
 #pragma unroll
     for (int x = 0; x < N; ++x) r[x] = f2u(u2f(r[x]) + wr[DIR * x]);
-  } else if (a.table != nullptr) {
-#pragma unroll
-    for (int x = 0; x < N; ++x) r[x] = f2u(u2f(r[x]) + far);
   }
 }
 

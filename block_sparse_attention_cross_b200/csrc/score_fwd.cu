@@ -37,24 +37,25 @@ constexpr int kLaunchRegs = 168;
 constexpr uint32_t kSoftmaxRegs = 192;
 constexpr uint32_t kControlRegs = 120;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
-constexpr int kProducer0 = 8, kMma = 9, kProducer1 = 11;
+constexpr int kProducer0 = 8, kMma = 9, kWindow = 10, kProducer1 = 11;
 constexpr uint32_t kTmemCols = 512;
 // The reference maximum is raised, and O rescaled, only when a tile's maximum
 // exceeds it by more than this many log2 units: P stays below 2^64.
 constexpr float kRescaleThreshold = 64.0f;
-constexpr int kMaxPackedTable = 8;   // heads of a packed tile with a table (windows in shared memory)
+constexpr int kMaxPackedTable = 4;   // heads of a packed tile with a table (windows in shared memory, two buffers)
 
 template <int D>
 struct Layout {
   static constexpr uint32_t BOX = TILE * 64 * 2;         // 128 rows x 64 columns, one swizzle span
   static constexpr uint32_t TBYTES = TILE * D * 2;       // one Q, K or V tile
-  static constexpr uint32_t WIN = kMaxPackedTable * 256 * 4;   // bias windows of one step
+  static constexpr uint32_t WIN = 2 * kMaxPackedTable * 256 * 4;   // the table's values in a tile pair's offsets, two buffers
   static constexpr int RING = D == 128 ? 2 : 4;          // K/V tiles per slot
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_RING = 2 * TBYTES;
-  static constexpr uint32_t OFF_WIN = OFF_RING + 2 * RING * TBYTES;   // [2 slots][WIN]
+  static constexpr uint32_t OFF_WIN = OFF_RING + 2 * RING * TBYTES;   // [2 slots][2 buffers][WIN / 2]
   static constexpr uint32_t OFF_CTRL = OFF_WIN + 2 * WIN;
-  static constexpr uint32_t SMEM = OFF_CTRL + 1024 + 1024;
+  static constexpr uint32_t CTRL = 1024;
+  static constexpr uint32_t SMEM = OFF_CTRL + CTRL + 1024;   // + alignment slack
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -65,6 +66,8 @@ struct Ctrl {
   uint64_t s_full[2], p_full[2];
   uint64_t o_full[2], o_free[2];
   uint64_t sync[2];     // the 128 softmax threads of a slot
+  uint64_t win_full[2][2], win_empty[2][2];
+  WindowInfo win_info[2][2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -116,47 +119,69 @@ __device__ __forceinline__ bool walk_start(const FwdArgs& f, int t, Walk& w) {
   return key_start(f.a, w.hx, w.qb, lo, w.hi, w);
 }
 
-// The producer's and the MMA warp's position: key tiles of this slot's
-// non-empty tiles, one after the other.
+// Tile of slot c in round `round` of n slots: the slots take turns from the
+// front and from the back, so that a slot that drew a long walk in one round
+// draws a short one in the next.  T or more: none.
+__device__ __forceinline__ int tile_of(int round, int c, int n) {
+  return round * n + ((round & 1) ? n - 1 - c : c);
+}
+
+// A role's position: key tiles of this slot's non-empty tiles, one after the other.
 struct Cursor {
   Walk w;
-  int t;
+  int round, slot;
   bool first, done;
 };
 
-__device__ __forceinline__ void cursor_seek(const FwdArgs& f, Cursor& c, int stride) {
-  while (c.t < f.T) {
-    if (walk_start(f, c.t, c.w)) {
+__device__ __forceinline__ void cursor_seek(const FwdArgs& f, Cursor& c) {
+  const int n = 2 * gridDim.x;
+  for (; c.round * n < f.T; ++c.round) {
+    const int t = tile_of(c.round, c.slot, n);
+    if (t < f.T && walk_start(f, t, c.w)) {
       c.first = true;
       return;
     }
-    c.t += stride;
   }
   c.done = true;
 }
 
-__device__ __forceinline__ void cursor_next(const FwdArgs& f, Cursor& c, int stride) {
+__device__ __forceinline__ void cursor_init(const FwdArgs& f, Cursor& c, int s) {
+  c.slot = blockIdx.x + s * gridDim.x;
+  c.round = 0;
+  c.done = false;
+  cursor_seek(f, c);
+}
+
+__device__ __forceinline__ void cursor_next(const FwdArgs& f, Cursor& c) {
   if (c.w.next >= 0) {
     c.first = false;
     key_next(f.a, c.w.hx, c.w.qb, c.w);
   } else {
-    c.t += stride;
-    cursor_seek(f, c, stride);
+    ++c.round;
+    cursor_seek(f, c);
   }
 }
 
-template <int D>
+// Beside the ScoreForm bits: capped scores without a bias and with a cap of
+// at most kBoundedCap need no maximum.
+constexpr int kBounded = 4;
+// Largest cap in log2 units that goes without a maximum: probabilities
+// 2^score lie in 2^+-80, their sums over 2^24 keys and their products with V
+// (|v| < 2^20) inside fp32, and bf16 has fp32's exponents.
+constexpr float kBoundedCap = 80.f;
+
+template <int D, int F>
 __global__ void __launch_bounds__(kThreads, 1)
     k_score_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdArgs f) {
   using L = Layout<D>;
   constexpr int R = L::RING;
+  static_assert(sizeof(Ctrl<R>) <= L::CTRL, "control block");
   const ScoreArgs& a = f.a;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Ctrl<R>* c = reinterpret_cast<Ctrl<R>*>(smem + L::OFF_CTRL);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int stride = 2 * gridDim.x;
 
   if (tid == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -171,6 +196,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c->o_full[s], 1);
       mbar_init(&c->o_free[s], 128);
       mbar_init(&c->sync[s], 128);
+      for (int e = 0; e < 2; ++e) {
+        mbar_init(&c->win_full[s][e], 32);
+        mbar_init(&c->win_empty[s][e], 128);
+      }
     }
     mbar_init(&c->drain, 1);
     c->abort = 0;
@@ -193,9 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ===================== TMA producer of one slot ===========================
     const int s = warp == kProducer1;
     Cursor cu;
-    cu.t = blockIdx.x + s * gridDim.x;
-    cu.done = false;
-    cursor_seek(f, cu, stride);
+    cursor_init(f, cu, s);
     uint32_t g = 0;
     int qf = 0;
     bool ok = true;
@@ -227,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         &c->ring_full[s][e], pol);
         ++g;
       }
-      cursor_next(f, cu, stride);
+      cursor_next(f, cu);
     }
     if (lane == 0) {
       if (!ok) {
@@ -246,11 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Per key tile of a slot: S, then (once the probabilities are stored) the
     // second product and the slot's next S; the slots are served in turn.
     Cursor cu0, cu1;
-    cu0.t = blockIdx.x;
-    cu1.t = blockIdx.x + gridDim.x;
-    cu0.done = cu1.done = false;
-    cursor_seek(f, cu0, stride);
-    cursor_seek(f, cu1, stride);
+    cursor_init(f, cu0, 0);
+    cursor_init(f, cu1, 1);
     constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, TILE, false);
     constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D, true);
     uint32_t g0 = 0, g1 = 0, gb0 = 0, gb1 = 0;
@@ -299,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (cu.w.next < 0) mma_commit_w(&c->o_full[s]);
       ++g;
       ++gb;
-      cursor_next(f, cu, stride);
+      cursor_next(f, cu);
       return cu.done ? true : issue_s(s_c);
     };
     bool due0 = false, due1 = false;
@@ -331,6 +355,45 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mma_commit_w(&c->drain);
     mbar_wait(&c->drain, 0, nullptr, a.spin_ns);
+  } else if (warp == kWindow) {
+    // ===================== the table's windows ================================
+    // Both slots' next windows, each filled as soon as its buffer is free
+    // (polled, so that no slot waits for the other).
+    if ((F & kBias) && a.table != nullptr) {
+      Cursor cu[2];
+      uint32_t n[2] = {0, 0};
+      cursor_init(f, cu[0], 0);
+      cursor_init(f, cu[1], 1);
+      bool ok = true, corrupt = false;
+      uint64_t since = globaltimer_ns();
+      while (ok && !(cu[0].done && cu[1].done)) {
+        bool moved = false;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (cu[s].done) continue;
+          const uint32_t e = n[s] & 1;
+          if (!__all_sync(0xffffffffu, mbar_test_wait(&c->win_empty[s][e], ((n[s] >> 1) & 1) ^ 1))) continue;
+          const Walk& w = cu[s].w;
+          const int p0 = a.q_start[w.b] + (a.packed ? 0 : w.qb * TILE), p1 = p0 + (a.packed ? a.Nq : TILE) - 1;
+          if (is_near(a, w.kb * TILE, p0, p1))
+            fill_window(a, a.packed ? w.hx * a.G : w.hx, a.packed ? a.G : 1, w.kb * TILE - p1,
+                        reinterpret_cast<float*>(smem + L::OFF_WIN + s * L::WIN + e * (L::WIN / 2)), nullptr,
+                        &c->win_info[s][e], &corrupt);
+          mbar_arrive(&c->win_full[s][e]);
+          ++n[s];
+          cursor_next(f, cu[s]);
+          moved = true;
+        }
+        const uint64_t now = globaltimer_ns();
+        if (moved) since = now;
+        else ok = __all_sync(0xffffffffu, now - since <= a.spin_ns && *static_cast<volatile int*>(&c->abort) == 0);
+      }
+      if (!ok) {
+        c->abort = 1;
+        report_status(a.status, CALIBATT_E_TIMEOUT);
+      }
+      if (corrupt) report_status(a.status, CALIBATT_E_CORRUPT);
+    }
   } else if (warp < 8) {
     // ===================== softmax warpgroups =================================
     regs_inc<kSoftmaxRegs>();
@@ -338,12 +401,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = w4 * 32 + lane;
     const uint32_t t_s = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + slot * 256;
     const uint32_t t_o = t_s + 128;
-    float* win = reinterpret_cast<float*>(smem + L::OFF_WIN + slot * L::WIN);
-    // Scores in log2 units.  Without a cap or bias the scale is folded into
-    // the exponential's FFMA; otherwise the transforms apply it.
-    const bool xform = a.cap > 0.f || a.slopes != nullptr || a.table != nullptr;
-    const float c2 = xform ? 1.f : a.scale * kLog2e;
+    // Scores are in log2 units.
     const ScoreTerms terms = score_terms(a);
+    const float c2 = F == 0 ? terms.sc : 1.f;   // plain scores: the scale is folded into the exponent
     const uint64_t c2x2 = f2pack(c2, c2);
     uint32_t gb = 0;
     int tiles = 0;
@@ -357,7 +417,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       sync_phase ^= 1;
       return static_cast<bool>(__all_sync(0xffffffffu, w));
     };
-    for (int t = blockIdx.x + slot * gridDim.x; ok && t < f.T; t += stride) {
+    const int slots = 2 * gridDim.x;
+    for (int round = 0; ok && round * slots < f.T; ++round) {
+      const int t = tile_of(round, blockIdx.x + slot * gridDim.x, slots);
+      if (t >= f.T) continue;
       Walk w;
       const bool any = walk_start(f, t, w);
       // this thread's row
@@ -397,52 +460,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const __nv_bfloat16* tab =
           reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
       float far_lo = 0.f, far_hi = 0.f;
-      if (a.table != nullptr) {
+      if ((F & kBias) && a.table != nullptr) {
         far_lo = __bfloat162float(tab[score_bucket(a, -a.R, &corrupt)]) * kLog2e;
         far_hi = __bfloat162float(tab[score_bucket(a, a.R, &corrupt)]) * kLog2e;
       }
-      float m = -INFINITY, l = 0.f, s_best = -INFINITY;
+      float m = F & kBounded ? 0.f : -INFINITY, l = 0.f;
+      float best = F & kBounded ? 0.f : -INFINITY;   // kBounded: largest probability; else largest score
       bool row_bad = false;
+      const bool work = __any_sync(0xffffffffu, live);   // few queries: warps without a row only keep the pace
       for (bool first = true;; first = false, ++gb) {
         const int k0 = w.kb * TILE;
         const bool edge = k0 < tr.z || k0 + TILE > tr.w;
-        const bool near = a.table != nullptr && k0 - p1 < a.R && k0 + TILE - 1 - p0 > -a.R;
-        if (near) {
-          // The table's values of the offsets k0 - p1 ... k0 + 127 - p0 of
-          // this tile, per head: 255 values, read with the row's own shift.
-          if (!(ok = slot_sync())) break;   // the previous window is read
-          const int heads = a.packed ? a.G : 1, h0 = a.packed ? w.hx * a.G : w.hx;
-          const int len = TILE + p1 - p0;
-          for (int x = row; x < len; x += TILE) {
-            const int n = score_bucket(a, k0 - p1 + x, &corrupt);
-            for (int g = 0; g < heads; ++g)
-              win[g * 256 + x] = kLog2e * __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(
-                                              a.table)[static_cast<size_t>(h0 + g) * a.n_buckets + n]);
-          }
-          if (!(ok = slot_sync())) break;
-        }
-        const bool got = mbar_wait(&c->s_full[slot], gb & 1, &c->abort, a.spin_ns);
+        bool got = mbar_wait(&c->s_full[slot], gb & 1, &c->abort, a.spin_ns);
+        if ((F & kBias) && got && a.table != nullptr)
+          got = mbar_wait(&c->win_full[slot][gb & 1], (gb >> 1) & 1, &c->abort, a.spin_ns);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
         tc_fence_after();
-        uint32_t r[TILE];
-#pragma unroll
-        for (int q4 = 0; q4 < TILE / 32; ++q4)
-          tmem_ld32(t_s + q4 * 32, *reinterpret_cast<uint32_t(*)[32]>(&r[q4 * 32]));
-        tmem_ld_wait();
-        reg_fence(r);
-        if (xform) {
-          const float* wr = win + (a.packed ? min(row / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
-          float none[TILE];
-          score_columns<1, false>(a, terms, r, none, slope, static_cast<float>(k0 - p), near, wr,
-                                  k0 > p1 ? far_hi : far_lo);
-        }
+        const int e0 = vis.x - k0, e1 = vis.y - k0;   // columns of the row's interval
         if (edge) {
-          // keys outside the row's interval
-          const int e0 = vis.x - k0, e1 = vis.y - k0;
-#pragma unroll
-          for (int x = 0; x < TILE; ++x)
-            if (x < e0 || x >= e1) r[x] = f2u(-INFINITY);
           // A probability of 0 does not silence a NaN or infinity in V: rows of
           // the V tile that hold one are zeroed before the second product, and
           // the query rows that see such a key become NaN.
@@ -452,13 +488,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           uint8_t* vrow = smem + L::OFF_RING + (slot * R + ge % R) * L::TBYTES + row * 128;
           bool bad = false;
-#pragma unroll
+#pragma unroll 1
           for (int x = 0; x < D / 64; ++x) bad |= clean_box_row(vrow + x * L::BOX, row);
           const uint32_t bw = __ballot_sync(0xffffffffu, bad);
           if (lane == 0) c->bad[slot][w4] = bw;
           fence_proxy_async_smem();
           if (!(ok = slot_sync())) break;
-#pragma unroll
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             // keys 32 q ... 32 q + 31 of the tile that this row sees
             const int s0 = min(max(e0 - 32 * q, 0), 32), s1 = min(max(e1 - 32 * q, 0), 32);
@@ -468,64 +504,131 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (!(ok = slot_sync())) break;
         }
-        float mx0 = u2f(r[0]), mx1 = u2f(r[1]), mx2 = u2f(r[2]), mx3 = u2f(r[3]);
+        if (work) {
+        // Both passes go over the tile in chunks of 32 columns, the next chunk
+        // loaded while the present one is worked on, in loops that are not
+        // unrolled: with all 128 columns unrolled, the bias and cap code that
+        // a call skips pushed the warps into instruction-cache misses (3.3
+        // stalled warps an issue), at half the speed.
+        const bool near = (F & kBias) && is_near(a, k0, p0, p1);
+        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN + slot * L::WIN + (gb & 1) * (L::WIN / 2)) +
+                          (a.packed ? min(row / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
+        const bool window = near && c->win_info[slot][gb & 1].cuts > 0;
+        const float flat = near ? (window ? 0.f : wr[0]) : k0 > p1 ? far_hi : far_lo;   // 0 without a table
+        const int side = k0 >= p1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0;
+        auto mask = [&](uint32_t (&r)[32], int ch) {
+          const int c0 = e0 - 32 * ch, c1 = e1 - 32 * ch;
 #pragma unroll
-        for (int x = 4; x + 8 <= TILE; x += 8) {
-          mx0 = fmax3(mx0, u2f(r[x + 0]), u2f(r[x + 1]));
-          mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
-          mx2 = fmax3(mx2, u2f(r[x + 4]), u2f(r[x + 5]));
-          mx3 = fmax3(mx3, u2f(r[x + 6]), u2f(r[x + 7]));
-        }
-        mx0 = fmax3(mx0, u2f(r[TILE - 4]), u2f(r[TILE - 3]));
-        mx1 = fmax3(mx1, u2f(r[TILE - 2]), u2f(r[TILE - 1]));
-        const float bmax = fmax3(mx0, mx1, fmaxf(mx2, mx3));
-        s_best = fmaxf(s_best, bmax);
-        // The reference: the first tile's maximum, raised (and O and l
-        // rescaled) only by more than the threshold.  While a row has seen
-        // nothing it is -inf and the exponent's shift 0.
+          for (int x = 0; x < 32; ++x)
+            if (x < c0 || x >= c1) r[x] = f2u(-INFINITY);
+        };
+        auto transform = [&](uint32_t (&r)[32], int ch) {
+          float none[32];
+          score_columns<F & 3, 1, false>(a, terms, r, none, slope, static_cast<float>(k0 + 32 * ch - p), side, window,
+                                         wr + 32 * ch, flat, edge);
+        };
+        uint32_t ra[32], rb[32];
         float alpha = 1.f;
         bool rescale = false;
-        const float m_cand = bmax * c2;
-        if (first) {
-          m = m_cand;
-        } else {
-          const bool raise = m_cand > m + kRescaleThreshold;
-          rescale = __any_sync(0xffffffffu, raise);
-          if (raise) {
-            alpha = ex2_approx(m - m_cand);
-            m = m_cand;
+        if (!(F & kBounded)) {
+          // First pass: (transformed) scores and the tile's maximum.
+          float mx0 = -INFINITY, mx1 = -INFINITY;
+          auto scan = [&](uint32_t (&r)[32], int ch) {
+            if (F != 0) transform(r, ch);
+            if (edge) mask(r, ch);
+#pragma unroll
+            for (int x = 0; x < 32; x += 4) {
+              mx0 = fmax3(mx0, u2f(r[x]), u2f(r[x + 1]));
+              mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
+            }
+            if (F != 0 || edge) tmem_st32(t_s + ch * 32, r);
+          };
+          tmem_ld32(t_s, ra);
+          tmem_ld_wait();
+          reg_fence(ra);
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ch += 2) {
+            tmem_ld32(t_s + ch * 32 + 32, rb);
+            scan(ra, ch);
+            tmem_ld_wait();
+            reg_fence(rb);
+            if (ch == 0) tmem_ld32(t_s + 64, ra);
+            scan(rb, ch + 1);
+            tmem_ld_wait();
+            reg_fence(ra);
           }
+          const float bmax = fmaxf(mx0, mx1);
+          best = fmaxf(best, bmax);
+          // The reference: the first tile's maximum, raised (and O and l
+          // rescaled) only by more than the threshold.  While a row has seen
+          // nothing it is -inf and the exponent's shift 0.
+          const float m_cand = bmax * c2;
+          if (first) {
+            m = m_cand;
+          } else {
+            const bool raise = m_cand > m + kRescaleThreshold;
+            rescale = __any_sync(0xffffffffu, raise);
+            if (raise) {
+              alpha = ex2_approx(m - m_cand);
+              m = m_cand;
+            }
+          }
+          if (F != 0 || edge) tmem_st_wait();
         }
+        if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[slot][gb & 1]);
+        // Second pass: probabilities, stored as bf16 pairs over the scores
+        // already read, and their fp32 sum.
         const float neg = m == -INFINITY ? 0.f : -m;
         const uint64_t negm = f2pack(neg, neg);
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-#pragma unroll
-        for (int c16 = 0; c16 < TILE / 32; ++c16) {
+        float pm0 = 0.f, pm1 = 0.f;
+        auto expo = [&](uint32_t (&r)[32], int ch) {
+          if (F & kBounded) {
+            transform(r, ch);
+            if (edge) mask(r, ch);
+          }
           uint32_t pk[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            const int e = c16 * 32 + 2 * x;
-            const uint64_t y = ffma2(f2pack(u2f(r[e]), u2f(r[e + 1])), c2x2, negm);
+            uint64_t y = pair_of(r, 2 * x);
+            if (!(F & kBounded)) y = ffma2(y, c2x2, negm);
             float xl, xh;
             f2unpack(y, xl, xh);
-            const uint64_t pv = f2pack(ex2_approx(xl), ex2_approx(xh));
+            xl = ex2_approx(xl);
+            xh = ex2_approx(xh);
+            const uint64_t pv = f2pack(xl, xh);
             if (x & 1) acc1 = fadd2(acc1, pv); else acc0 = fadd2(acc0, pv);
-            float pl, ph;
-            f2unpack(pv, pl, ph);
-            pk[x] = pack_bf16x2(pl, ph);
+            if (F & kBounded) {
+              if (x & 1) pm1 = fmax3(pm1, xl, xh); else pm0 = fmax3(pm0, xl, xh);
+            }
+            pk[x] = pack_bf16x2(xl, xh);
           }
-          tmem_st16(t_s + c16 * 16, pk);
+          tmem_st16(t_s + ch * 16, pk);
+        };
+        tmem_ld32(t_s, ra);
+        tmem_ld_wait();
+        reg_fence(ra);
+#pragma unroll 1
+        for (int ch = 0; ch < 4; ch += 2) {
+          tmem_ld32(t_s + ch * 32 + 32, rb);
+          expo(ra, ch);
+          tmem_ld_wait();
+          reg_fence(rb);
+          if (ch == 0) tmem_ld32(t_s + 64, ra);
+          expo(rb, ch + 1);
+          tmem_ld_wait();
+          reg_fence(ra);
         }
+        if (F & kBounded) best = fmaxf(best, fmaxf(pm0, pm1));
         if (rescale) {
-#pragma unroll
+#pragma unroll 1
           for (int q4 = 0; q4 < D / 32; ++q4) {
-            uint32_t ro[32];
-            tmem_ld32(t_o + q4 * 32, ro);
+            tmem_ld32(t_o + q4 * 32, ra);
             tmem_ld_wait();
-            reg_fence(ro);
+            reg_fence(ra);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) ro[x] = f2u(u2f(ro[x]) * alpha);
-            tmem_st32(t_o + q4 * 32, ro);
+            for (int x = 0; x < 32; ++x) ra[x] = f2u(u2f(ra[x]) * alpha);
+            tmem_st32(t_o + q4 * 32, ra);
           }
         }
         float a0, a1, b0, b1;
@@ -533,6 +636,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         f2unpack(acc1, b0, b1);
         l = l * alpha + ((a0 + a1) + (b0 + b1));
         tmem_st_wait();
+        } else if ((F & kBias) && a.table != nullptr) {
+          mbar_arrive(&c->win_empty[slot][gb & 1]);
+        }
         tc_fence_before();
         mbar_arrive(&c->p_full[slot]);
         if (w.next < 0) { ++gb; break; }
@@ -542,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- epilogue: O / l, LSE.  As in the block-sparse forward, the
       // rounding error of the row's largest probability moves into the
       // normaliser, so that a row with one dominant key returns its value.
-      const float p_best = ex2_approx(fmaf(s_best, c2, -m));
+      const float p_best = F & kBounded ? best : ex2_approx(fmaf(best, c2, -m));
       const float corr = __uint_as_float(pack_bf16x2(p_best, 0.f) << 16) - p_best;
       ok = __all_sync(0xffffffffu, mbar_wait(&c->o_full[slot], tiles & 1, &c->abort, a.spin_ns));
       if (!ok) break;
@@ -552,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float row_lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       if (a.splits > 1) {
         float* po = a.part_o + (orow * a.splits + w.sp) * D;
-#pragma unroll
+#pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t ro[32];
           tmem_ld32(t_o + q4 * 32, ro);
@@ -568,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (live) a.part_lse[orow * a.splits + w.sp] = row_lse;
       } else {
-#pragma unroll
+#pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t ro[32];
           tmem_ld32(t_o + q4 * 32, ro);
@@ -643,7 +749,7 @@ __global__ void __launch_bounds__(128) k_score_join(const ScoreArgs a) {
   if (lane == 0 && a.lse != nullptr) a.lse[r] = nan ? NAN : l == 0.f ? -INFINITY : mx + logf(l);
 }
 
-template <int D>
+template <int D, int F>
 int launch(const ScoreArgs& a, int sms, cudaStream_t s) {
   FwdArgs f;
   f.a = a;
@@ -662,7 +768,7 @@ int launch(const ScoreArgs& a, int sms, cudaStream_t s) {
   if ((rc = make_tmap4_bf16(&tq, a.q, a.B, a.H, a.Nq, D, a.packed ? a.Nq : TILE, a.packed ? a.G : 1))) return rc;
   if ((rc = make_tmap4_bf16(&tk, a.k, a.B, a.Hkv, a.Nk, D, TILE, 1))) return rc;
   if ((rc = make_tmap4_bf16(&tv, a.v, a.B, a.Hkv, a.Nk, D, TILE, 1))) return rc;
-  auto kern = k_score_fwd<D>;
+  auto kern = k_score_fwd<D, F>;
   static std::atomic<bool> done[kMaxDevices];
   if ((rc = configure_kernel(reinterpret_cast<const void*>(kern), done, Layout<D>::SMEM, kLaunchRegs, "k_score_fwd")))
     return rc;
@@ -700,7 +806,16 @@ int score_splits(int B, int heads, int nq_tiles, int nkb) {
 int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s) {
   int sms = 0;
   if (int rc = device_sms(&sms)) return rc;
-  return d == 128 ? launch<128>(a, sms, s) : launch<64>(a, sms, s);
+  const bool bias = a.slopes != nullptr || a.table != nullptr;
+  const int form = (a.cap > 0.f ? kCap : 0) | (bias ? kBias : 0) |
+                   (a.cap > 0.f && !bias && a.cap * kLog2e <= kBoundedCap ? kBounded : 0);
+  switch (form) {
+    case 0: return d == 128 ? launch<128, 0>(a, sms, s) : launch<64, 0>(a, sms, s);
+    case kCap: return d == 128 ? launch<128, kCap>(a, sms, s) : launch<64, kCap>(a, sms, s);
+    case kCap | kBounded: return d == 128 ? launch<128, kCap | kBounded>(a, sms, s) : launch<64, kCap | kBounded>(a, sms, s);
+    case kBias: return d == 128 ? launch<128, kBias>(a, sms, s) : launch<64, kBias>(a, sms, s);
+    default: return d == 128 ? launch<128, kCap | kBias>(a, sms, s) : launch<64, kCap | kBias>(a, sms, s);
+  }
 }
 
 }  // namespace calibatt
