@@ -398,9 +398,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // column x: query 64 half + x, offset j - p falls with x
         const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (t & 1) * 256 + row + TILE - 1 - half * 64;
         const bool window = near && c->win_info[t & 1].cuts > 0;
-        score_columns<F, -1, true>(a, terms, r, pf, slope, static_cast<float>(j - p0 - half * 64),
-                                k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
-                                near ? (window ? 0.f : wr[0]) : far, edge);
+        const ScoreBias bias{slope, static_cast<float>(j - p0 - half * 64),
+                             k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
+                             near ? (window ? 0.f : wr[0]) : far};
+        score_columns<F, -1, true, true>(a, terms, r, pf, bias, edge);
         if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[t & 1]);
       } else {
 #pragma unroll
@@ -798,9 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (wt & 1) * 256 + TILE - 1 - row + half * 64;
         const bool window = near && c->win_info[wt & 1].cuts > 0;
         float none[64];
-        score_columns<F, 1, false>(a, terms, r, none, slope, static_cast<float>(k0 + half * 64 - p0 - row),
-                                k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
-                                near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo, edge);
+        const ScoreBias bias{slope, static_cast<float>(k0 + half * 64 - p0 - row),
+                             k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
+                             near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo};
+        score_columns<F, 1, false, true>(a, terms, r, none, bias, edge);
         if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[wt & 1]);
       }
       if (edge) {
@@ -868,9 +870,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (xform) {
         const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (wt & 1) * 256 + TILE - 1 - row + half * 64;
         const bool window = near && c->win_info[wt & 1].cuts > 0;
-        score_columns<F, 1, true>(a, terms, r, f, slope, static_cast<float>(k0 + half * 64 - p0 - row),
-                                k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
-                                near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo, edge);
+        const ScoreBias bias{slope, static_cast<float>(k0 + half * 64 - p0 - row),
+                             k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
+                             near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo};
+        score_columns<F, 1, true, true>(a, terms, r, f, bias, edge);
       } else {
 #pragma unroll
         for (int x = 0; x < 64; ++x) f[x] = 1.f;

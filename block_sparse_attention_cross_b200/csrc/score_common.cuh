@@ -222,8 +222,8 @@ __device__ __forceinline__ void fill_window(const ScoreArgs& a, int h0, int head
 // elsewhere cap - 2 cap / (1 + e^(2x)), two MUFU operations a score, right at
 // both ends.  Both stay within 3e-7 of the cap.  The polynomial leaves the
 // MUFU, which bounds the softmax, to the exponentials.  A row chooses by its
-// own scores, and in a tile that the mask cuts (`exact`) always takes the
-// second form, so no other row and no masked place changes a bit of it.
+// own scores, and where the mask cuts it (`exact`) always takes the second
+// form, so no other row and no masked place changes a bit of it.
 struct ScoreTerms {
   float sc;                  // scale log2e
   float capA, kcap, small;   // cap log2e; 2 log2e scale / cap; largest |s| for the polynomial
@@ -258,57 +258,74 @@ __device__ __forceinline__ void set_pair(uint32_t* r, int x, uint64_t v) {
   r[x + 1] = f2u(hi);
 }
 
-// DIR = 1: the columns are keys, off0 the first one's offset j - p; DIR = -1:
-// the columns are queries.  side: +1 / -1 where every offset of the tile is >=
-// 0 / <= 0 (the distance is linear then), 0 otherwise.  window: the table's
-// value of column x is wr[DIR x], otherwise `flat` is added.  With FACTOR, f
-// becomes the derivative of the cap.
 // F: which terms the kernel was built for.  A kernel carries the code of its
 // own terms only: code that a call skips costs instruction-cache misses (all
 // terms in one kernel ran plain far tiles of a table at half the speed).
 enum ScoreForm { kCap = 1, kBias = 2 };
-template <int F, int DIR, bool FACTOR, int N>
+
+// What a tile pair adds to the scores of one thread's row.
+struct ScoreBias {
+  float slope, off0;   // distance: -slope |off0 + DIR x| at column x
+  int side;            // +1 / -1: every offset of the tile is >= 0 / <= 0, the distance is linear; 0: neither
+  bool window;         // the table's value at column x is wr[DIR x], otherwise `flat` everywhere
+  const float* wr;
+  float flat;          // 0 without a table
+};
+
+// Largest |score| of the row.  (A NaN is not seen; every form passes it on.)
+template <int N>
+__device__ __forceinline__ float score_extent(const uint32_t (&r)[N]) {
+  float big0 = 0.f, big1 = 0.f;
+#pragma unroll
+  for (int x = 0; x < N; x += 4) {
+    big0 = fmax3(big0, fabsf(u2f(r[x])), fabsf(u2f(r[x + 1])));
+    big1 = fmax3(big1, fabsf(u2f(r[x + 2])), fabsf(u2f(r[x + 3])));
+  }
+  return fmaxf(big0, big1);
+}
+
+// The capped score by the polynomial, plus `shift`; f: the cap's derivative.
+template <bool FACTOR, int N>
+__device__ __forceinline__ void cap_polynomial(const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N], float shift) {
+  const uint64_t c0 = f2pack(t.c[0], t.c[0]), c1 = f2pack(t.c[1], t.c[1]), c2 = f2pack(t.c[2], t.c[2]),
+                 c3 = f2pack(t.c[3], t.c[3]), c4 = f2pack(t.c[4], t.c[4]), shift2 = f2pack(shift, shift);
+  const uint64_t iv = f2pack(t.inv, t.inv), one = f2pack(1.f, 1.f), neg = f2pack(-1.f, -1.f);
+#pragma unroll
+  for (int x = 0; x < N; x += 2) {
+    const uint64_t s = pair_of(r, x), v = fmul2(s, s);
+    const uint64_t q = ffma2(ffma2(ffma2(ffma2(c4, v, c3), v, c2), v, c1), v, c0);
+    set_pair(r, x, ffma2(s, q, shift2));
+    if (FACTOR) {
+      const uint64_t th = fmul2(fmul2(s, q), iv);
+      f2unpack(ffma2(fmul2(th, neg), th, one), f[x], f[x + 1]);
+    }
+  }
+}
+template <bool FACTOR, int N>
+__device__ __forceinline__ void cap_mufu(const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N], float shift) {
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    const float rc = rcp_approx(1.f + ex2_approx(u2f(r[x]) * t.kcap));
+    if (FACTOR) f[x] = 4.f * (rc - rc * rc);
+    r[x] = f2u(fmaf(-2.f * t.capA, rc, t.capA) + shift);
+  }
+}
+
+// The score function.  DIR = 1: the columns are keys; DIR = -1: queries.
+// BENT: the distance may pass 0 inside the tile; exact: see above.
+template <int F, int DIR, bool FACTOR, bool BENT, int N>
 __device__ __forceinline__ void score_columns(const ScoreArgs& a, const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N],
-                                              float slope, float off0, int side, bool window, const float* wr,
-                                              float flat, bool exact) {
+                                              const ScoreBias& b, bool exact) {
   // The constant part of the biases: the flat table value, and the distance
   // of column 0 where the distance is linear over the tile.
-  const bool linear = (F & kBias) && a.slopes != nullptr && side != 0;
-  const float sl = side > 0 ? -slope : slope;   // -slope |off0 + DIR x| = sl (off0 + DIR x)
-  const float shift = F & kBias ? (window ? 0.f : flat) + (linear ? sl * off0 : 0.f) : 0.f;
-  const uint64_t shift2 = f2pack(shift, shift);
+  const bool slopes = (F & kBias) && a.slopes != nullptr, linear = slopes && (!BENT || b.side != 0);
+  const float sl = b.side > 0 ? -b.slope : b.slope;   // -slope |off0 + DIR x| = sl (off0 + DIR x)
+  const float shift = F & kBias ? (b.window ? 0.f : b.flat) + (linear ? sl * b.off0 : 0.f) : 0.f;
   if (F & kCap) {
-    float big = 0.f, big1 = 0.f;
-#pragma unroll
-    for (int x = 0; x < N; x += 4) {
-      big = fmax3(big, fabsf(u2f(r[x])), fabsf(u2f(r[x + 1])));
-      big1 = fmax3(big1, fabsf(u2f(r[x + 2])), fabsf(u2f(r[x + 3])));
-    }
-    // (a NaN is not seen by the maximum; both forms pass it on)
-    if (!exact && fmaxf(big, big1) <= t.small) {
-      const uint64_t c0 = f2pack(t.c[0], t.c[0]), c1 = f2pack(t.c[1], t.c[1]), c2 = f2pack(t.c[2], t.c[2]),
-                     c3 = f2pack(t.c[3], t.c[3]), c4 = f2pack(t.c[4], t.c[4]);
-      const uint64_t iv = f2pack(t.inv, t.inv), one = f2pack(1.f, 1.f), neg = f2pack(-1.f, -1.f);
-#pragma unroll
-      for (int x = 0; x < N; x += 2) {
-        const uint64_t s = pair_of(r, x), v = fmul2(s, s);
-        const uint64_t q = ffma2(ffma2(ffma2(ffma2(c4, v, c3), v, c2), v, c1), v, c0);
-        set_pair(r, x, ffma2(s, q, shift2));
-        if (FACTOR) {
-          const uint64_t th = fmul2(fmul2(s, q), iv);
-          f2unpack(ffma2(fmul2(th, neg), th, one), f[x], f[x + 1]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int x = 0; x < N; ++x) {
-        const float rc = rcp_approx(1.f + ex2_approx(u2f(r[x]) * t.kcap));
-        if (FACTOR) f[x] = 4.f * (rc - rc * rc);
-        r[x] = f2u(fmaf(-2.f * t.capA, rc, t.capA) + shift);
-      }
-    }
+    if (!exact && score_extent(r) <= t.small) cap_polynomial<FACTOR>(t, r, f, shift);
+    else cap_mufu<FACTOR>(t, r, f, shift);
   } else {
-    const uint64_t sc = f2pack(t.sc, t.sc);
+    const uint64_t sc = f2pack(t.sc, t.sc), shift2 = f2pack(shift, shift);
 #pragma unroll
     for (int x = 0; x < N; x += 2) set_pair(r, x, ffma2(pair_of(r, x), sc, shift2));
     if (FACTOR) {
@@ -320,13 +337,13 @@ __device__ __forceinline__ void score_columns(const ScoreArgs& a, const ScoreTer
   if (linear) {
 #pragma unroll
     for (int x = 0; x < N; ++x) r[x] = f2u(fmaf(sl, static_cast<float>(DIR * x), u2f(r[x])));
-  } else if (a.slopes != nullptr) {
+  } else if (BENT && slopes) {
 #pragma unroll
-    for (int x = 0; x < N; ++x) r[x] = f2u(fmaf(-slope, fabsf(off0 + static_cast<float>(DIR * x)), u2f(r[x])));
+    for (int x = 0; x < N; ++x) r[x] = f2u(fmaf(-b.slope, fabsf(b.off0 + static_cast<float>(DIR * x)), u2f(r[x])));
   }
-  if (window) {
+  if (b.window) {
 #pragma unroll
-    for (int x = 0; x < N; ++x) r[x] = f2u(u2f(r[x]) + wr[DIR * x]);
+    for (int x = 0; x < N; ++x) r[x] = f2u(u2f(r[x]) + b.wr[DIR * x]);
   }
 }
 

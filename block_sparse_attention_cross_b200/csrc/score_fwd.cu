@@ -65,13 +65,12 @@ struct Ctrl {
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_full[2];
   uint64_t o_full[2], o_free[2];
-  uint64_t sync[2];     // the 128 softmax threads of a slot
   uint64_t win_full[2][2], win_empty[2][2];
   WindowInfo win_info[2][2];
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
-  uint32_t bad[2][4];   // keys of a slot's V tile that hold a non-finite value
+  uint32_t bad[2][2][4];   // [slot][step & 1]: keys of a V tile that hold a non-finite value
 };
 
 struct FwdArgs {
@@ -170,6 +169,28 @@ constexpr int kBounded = 4;
 // (|v| < 2^20) inside fp32, and bf16 has fp32's exponents.
 constexpr float kBoundedCap = 80.f;
 
+// Columns below n of a chunk of 32, as bits.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Columns whose bit is 0 become `value`.
+__device__ __forceinline__ void keep_bits(uint32_t (&r)[32], uint32_t bits, float value) {
+#pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (!(bits & (1u << x))) r[x] = f2u(value);
+}
+
+// Row `row` of a V tile: zeroed where a 64-column box of it holds a NaN or an infinity; whether one did.
+template <int D>
+__device__ __noinline__ bool clean_row(uint8_t* tile, int row) {
+  bool bad = false;
+#pragma unroll 1
+  for (int x = 0; x < D / 64; ++x) bad |= clean_box_row(tile + x * TILE * 128 + row * 128, row);
+  fence_proxy_async_smem();
+  return bad;
+}
+
 template <int D, int F>
 __global__ void __launch_bounds__(kThreads, 1)
     k_score_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -195,7 +216,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c->p_full[s], 128);
       mbar_init(&c->o_full[s], 1);
       mbar_init(&c->o_free[s], 128);
-      mbar_init(&c->sync[s], 128);
       for (int e = 0; e < 2; ++e) {
         mbar_init(&c->win_full[s][e], 32);
         mbar_init(&c->win_empty[s][e], 128);
@@ -408,15 +428,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t gb = 0;
     int tiles = 0;
     bool ok = true, corrupt = false;
-    // Barrier among the slot's softmax threads, bounded like every wait here
-    // (a bar.sync would hang if another warp of the slot gave up).
-    uint32_t sync_phase = 0;
-    auto slot_sync = [&]() {
-      mbar_arrive(&c->sync[slot]);
-      const bool w = mbar_wait(&c->sync[slot], sync_phase, &c->abort, a.spin_ns);
-      sync_phase ^= 1;
-      return static_cast<bool>(__all_sync(0xffffffffu, w));
-    };
     const int slots = 2 * gridDim.x;
     for (int round = 0; ok && round * slots < f.T; ++round) {
       const int t = tile_of(round, blockIdx.x + slot * gridDim.x, slots);
@@ -467,6 +478,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = F & kBounded ? 0.f : -INFINITY, l = 0.f;
       float best = F & kBounded ? 0.f : -INFINITY;   // kBounded: largest probability; else largest score
       bool row_bad = false;
+      bool scanned = false;      // the step before this one listed bad keys
+      int seen0 = 0, seen1 = 0;  // and the row saw these columns of it
+      auto see_bad = [&](uint32_t step) {
+        if (!scanned) return;
+        scanned = false;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q)
+          row_bad |= (c->bad[slot][(step & 1) ^ 1][q] & bits_below(seen1 - 32 * q) & ~bits_below(seen0 - 32 * q)) != 0;
+      };
       const bool work = __any_sync(0xffffffffu, live);   // few queries: warps without a row only keep the pace
       for (bool first = true;; first = false, ++gb) {
         const int k0 = w.kb * TILE;
@@ -478,157 +498,156 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const int e0 = vis.x - k0, e1 = vis.y - k0;   // columns of the row's interval
+        see_bad(gb);
         if (edge) {
           // A probability of 0 does not silence a NaN or infinity in V: rows of
           // the V tile that hold one are zeroed before the second product, and
-          // the query rows that see such a key become NaN.
+          // the query rows that see such a key become NaN: the list of the
+          // keys is read at the next step, when every thread has written.
           const uint32_t ge = 2 * gb + 1;
           ok = __all_sync(0xffffffffu,
                           mbar_wait(&c->ring_full[slot][ge % R], (ge / R) & 1, &c->abort, a.spin_ns));
           if (!ok) break;
-          uint8_t* vrow = smem + L::OFF_RING + (slot * R + ge % R) * L::TBYTES + row * 128;
-          bool bad = false;
-#pragma unroll 1
-          for (int x = 0; x < D / 64; ++x) bad |= clean_box_row(vrow + x * L::BOX, row);
+          const bool bad = clean_row<D>(smem + L::OFF_RING + (slot * R + ge % R) * L::TBYTES, row);
           const uint32_t bw = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0) c->bad[slot][w4] = bw;
-          fence_proxy_async_smem();
-          if (!(ok = slot_sync())) break;
-#pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            // keys 32 q ... 32 q + 31 of the tile that this row sees
-            const int s0 = min(max(e0 - 32 * q, 0), 32), s1 = min(max(e1 - 32 * q, 0), 32);
-            const uint32_t below1 = s1 >= 32 ? 0xffffffffu : (1u << s1) - 1u;
-            const uint32_t below0 = s0 >= 32 ? 0xffffffffu : (1u << s0) - 1u;
-            row_bad |= (c->bad[slot][q] & below1 & ~below0) != 0;
-          }
-          if (!(ok = slot_sync())) break;
+          if (lane == 0) c->bad[slot][gb & 1][w4] = bw;
+          scanned = true;
+          seen0 = e0;
+          seen1 = e1;
         }
         if (work) {
-        // Both passes go over the tile in chunks of 32 columns, the next chunk
-        // loaded while the present one is worked on, in loops that are not
-        // unrolled: with all 128 columns unrolled, the bias and cap code that
-        // a call skips pushed the warps into instruction-cache misses (3.3
-        // stalled warps an issue), at half the speed.
+        // Both passes go over the tile in chunks of 32 columns, in loops that
+        // are not unrolled, and a tile that the mask cuts or where the distance
+        // passes 0 has loops of its own: a warp is mostly alone on its
+        // sub-partition, so instruction fetch bounds it, and instructions that
+        // the ordinary tiles skip cost them (masks inside their loops: plain
+        // scores 932 -> 1003 us, capped 1127 -> 1351 us at 24 heads of 8192
+        // tokens, d = 128; all 128 columns unrolled: 1573 us capped).
         const bool near = (F & kBias) && is_near(a, k0, p0, p1);
-        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN + slot * L::WIN + (gb & 1) * (L::WIN / 2)) +
-                          (a.packed ? min(row / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
-        const bool window = near && c->win_info[slot][gb & 1].cuts > 0;
-        const float flat = near ? (window ? 0.f : wr[0]) : k0 > p1 ? far_hi : far_lo;   // 0 without a table
-        const int side = k0 >= p1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0;
-        auto mask = [&](uint32_t (&r)[32], int ch) {
-          const int c0 = e0 - 32 * ch, c1 = e1 - 32 * ch;
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (x < c0 || x >= c1) r[x] = f2u(-INFINITY);
-        };
-        auto transform = [&](uint32_t (&r)[32], int ch) {
-          float none[32];
-          score_columns<F & 3, 1, false>(a, terms, r, none, slope, static_cast<float>(k0 + 32 * ch - p), side, window,
-                                         wr + 32 * ch, flat, edge);
-        };
-        uint32_t ra[32], rb[32];
+        ScoreBias bias = {};
+        if (F & kBias) {
+          bias.wr = reinterpret_cast<const float*>(smem + L::OFF_WIN + slot * L::WIN + (gb & 1) * (L::WIN / 2)) +
+                    (a.packed ? min(row / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
+          bias.window = near && c->win_info[slot][gb & 1].cuts > 0;
+          bias.flat = near ? (bias.window ? 0.f : bias.wr[0]) : k0 > p1 ? far_hi : far_lo;
+          bias.side = k0 >= p1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0;
+          bias.slope = slope;
+          bias.off0 = static_cast<float>(k0 - p);
+        }
         float alpha = 1.f;
         bool rescale = false;
-        if (!(F & kBounded)) {
-          // First pass: (transformed) scores and the tile's maximum.
-          float mx0 = -INFINITY, mx1 = -INFINITY;
-          auto scan = [&](uint32_t (&r)[32], int ch) {
-            if (F != 0) transform(r, ch);
-            if (edge) mask(r, ch);
-#pragma unroll
-            for (int x = 0; x < 32; x += 4) {
-              mx0 = fmax3(mx0, u2f(r[x]), u2f(r[x + 1]));
-              mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
-            }
-            if (F != 0 || edge) tmem_st32(t_s + ch * 32, r);
-          };
-          tmem_ld32(t_s, ra);
-          tmem_ld_wait();
-          reg_fence(ra);
-#pragma unroll 1
-          for (int ch = 0; ch < 4; ch += 2) {
-            tmem_ld32(t_s + ch * 32 + 32, rb);
-            scan(ra, ch);
-            tmem_ld_wait();
-            reg_fence(rb);
-            if (ch == 0) tmem_ld32(t_s + 64, ra);
-            scan(rb, ch + 1);
-            tmem_ld_wait();
-            reg_fence(ra);
-          }
-          const float bmax = fmaxf(mx0, mx1);
-          best = fmaxf(best, bmax);
-          // The reference: the first tile's maximum, raised (and O and l
-          // rescaled) only by more than the threshold.  While a row has seen
-          // nothing it is -inf and the exponent's shift 0.
-          const float m_cand = bmax * c2;
-          if (first) {
-            m = m_cand;
-          } else {
-            const bool raise = m_cand > m + kRescaleThreshold;
-            rescale = __any_sync(0xffffffffu, raise);
-            if (raise) {
-              alpha = ex2_approx(m - m_cand);
-              m = m_cand;
-            }
-          }
-          if (F != 0 || edge) tmem_st_wait();
-        }
-        if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[slot][gb & 1]);
-        // Second pass: probabilities, stored as bf16 pairs over the scores
-        // already read, and their fp32 sum.
-        const float neg = m == -INFINITY ? 0.f : -m;
-        const uint64_t negm = f2pack(neg, neg);
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-        float pm0 = 0.f, pm1 = 0.f;
-        auto expo = [&](uint32_t (&r)[32], int ch) {
-          if (F & kBounded) {
-            transform(r, ch);
-            if (edge) mask(r, ch);
-          }
-          uint32_t pk[16];
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            uint64_t y = pair_of(r, 2 * x);
-            if (!(F & kBounded)) y = ffma2(y, c2x2, negm);
-            float xl, xh;
-            f2unpack(y, xl, xh);
-            xl = ex2_approx(xl);
-            xh = ex2_approx(xh);
-            const uint64_t pv = f2pack(xl, xh);
-            if (x & 1) acc1 = fadd2(acc1, pv); else acc0 = fadd2(acc0, pv);
-            if (F & kBounded) {
-              if (x & 1) pm1 = fmax3(pm1, xl, xh); else pm0 = fmax3(pm0, xl, xh);
+        auto softmax = [&](auto cut_c) {
+          constexpr bool CUT = decltype(cut_c)::value != 0;
+          uint32_t r[32];
+          uint32_t dead = 0;   // chunks that no row of the warp sees
+          auto load = [&](int ch) {
+            tmem_ld32(t_s + ch * 32, r);
+            tmem_ld_wait();
+            reg_fence(r);
+          };
+          // log2 units, -inf where masked; false: no row of the warp sees the chunk
+          auto transform = [&](int ch) {
+            const uint32_t bits = CUT ? bits_below(e1 - 32 * ch) & ~bits_below(e0 - 32 * ch) : 0xffffffffu;
+            if (CUT && !__any_sync(0xffffffffu, bits != 0)) return false;
+            if (F != 0) {
+              ScoreBias at = bias;
+              at.off0 += static_cast<float>(32 * ch);
+              at.wr += 32 * ch;
+              float none[32];
+              score_columns<F & 3, 1, false, CUT>(a, terms, r, none, at, CUT && ~bits != 0);
             }
-            pk[x] = pack_bf16x2(xl, xh);
-          }
-          tmem_st16(t_s + ch * 16, pk);
-        };
-        tmem_ld32(t_s, ra);
-        tmem_ld_wait();
-        reg_fence(ra);
+            if (CUT) keep_bits(r, bits, -INFINITY);
+            return true;
+          };
+          if (!(F & kBounded)) {
+            // First pass: (transformed) scores and the tile's maximum.
+            float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
-        for (int ch = 0; ch < 4; ch += 2) {
-          tmem_ld32(t_s + ch * 32 + 32, rb);
-          expo(ra, ch);
-          tmem_ld_wait();
-          reg_fence(rb);
-          if (ch == 0) tmem_ld32(t_s + 64, ra);
-          expo(rb, ch + 1);
-          tmem_ld_wait();
-          reg_fence(ra);
-        }
-        if (F & kBounded) best = fmaxf(best, fmaxf(pm0, pm1));
+            for (int ch = 0; ch < 4; ++ch) {
+              load(ch);
+              if (!transform(ch)) {
+                dead |= 1u << ch;
+                continue;
+              }
+#pragma unroll
+              for (int x = 0; x < 32; x += 4) {
+                mx0 = fmax3(mx0, u2f(r[x]), u2f(r[x + 1]));
+                mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
+              }
+              if (F != 0 || CUT) tmem_st32(t_s + ch * 32, r);
+            }
+            const float bmax = fmaxf(mx0, mx1);
+            best = fmaxf(best, bmax);
+            // The reference: the first tile's maximum, raised (and O and l
+            // rescaled) only by more than the threshold.  While a row has seen
+            // nothing it is -inf and the exponent's shift 0.
+            const float m_cand = bmax * c2;
+            if (first) {
+              m = m_cand;
+            } else {
+              const bool raise = m_cand > m + kRescaleThreshold;
+              rescale = __any_sync(0xffffffffu, raise);
+              if (raise) {
+                alpha = ex2_approx(m - m_cand);
+                m = m_cand;
+              }
+            }
+            if (F != 0 || CUT) tmem_st_wait();
+          }
+          // Second pass: probabilities, stored as bf16 pairs over the scores
+          // already read, and their fp32 sum.
+          const float neg = m == -INFINITY ? 0.f : -m;
+          const uint64_t negm = f2pack(neg, neg);
+          float pm0 = 0.f, pm1 = 0.f;
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            uint32_t pk[16];
+            bool some = true;
+            if (!CUT || !((dead >> ch) & 1u)) {
+              load(ch);
+              if (F & kBounded) some = transform(ch);
+            } else {
+              some = false;
+            }
+            if (CUT && !some) {
+#pragma unroll
+              for (int x = 0; x < 16; ++x) pk[x] = 0;
+              tmem_st16(t_s + ch * 16, pk);
+              continue;
+            }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              uint64_t y = pair_of(r, 2 * x);
+              if (!(F & kBounded)) y = ffma2(y, c2x2, negm);
+              float xl, xh;
+              f2unpack(y, xl, xh);
+              xl = ex2_approx(xl);
+              xh = ex2_approx(xh);
+              const uint64_t pv = f2pack(xl, xh);
+              if (x & 1) acc1 = fadd2(acc1, pv); else acc0 = fadd2(acc0, pv);
+              if (F & kBounded) {
+                if (x & 1) pm1 = fmax3(pm1, xl, xh); else pm0 = fmax3(pm0, xl, xh);
+              }
+              pk[x] = pack_bf16x2(xl, xh);
+            }
+            tmem_st16(t_s + ch * 16, pk);
+          }
+          if (F & kBounded) best = fmaxf(best, fmaxf(pm0, pm1));
+        };
+        if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) softmax(IntC<1>{});
+        else softmax(IntC<0>{});
+        if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[slot][gb & 1]);
         if (rescale) {
 #pragma unroll 1
           for (int q4 = 0; q4 < D / 32; ++q4) {
-            tmem_ld32(t_o + q4 * 32, ra);
+            uint32_t ro[32];
+            tmem_ld32(t_o + q4 * 32, ro);
             tmem_ld_wait();
-            reg_fence(ra);
+            reg_fence(ro);
 #pragma unroll
-            for (int x = 0; x < 32; ++x) ra[x] = f2u(u2f(ra[x]) * alpha);
-            tmem_st32(t_o + q4 * 32, ra);
+            for (int x = 0; x < 32; ++x) ro[x] = f2u(u2f(ro[x]) * alpha);
+            tmem_st32(t_o + q4 * 32, ro);
           }
         }
         float a0, a1, b0, b1;
@@ -654,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++tiles;
       tc_fence_after();
+      see_bad(gb);
       const float inv_l = row_bad ? NAN : l == 0.f ? 0.f : 1.f / (l + corr);
       const float row_lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       if (a.splits > 1) {
