@@ -97,9 +97,11 @@ struct ScoreArgs {
   float* lse;               // [B, H, Nq] (forward: written, may be nullptr; backward: read)
   void* dtable;             // [H, n_buckets] or nullptr
   // workspace
-  int splits, packed;       // forward: splits of the key axis; packed: the G heads of a key head share a tile
-  float* part_o;            // [B, H, Nq, splits, d]
-  float* part_lse;          // [B, H, Nq, splits]
+  int splits, packed, few;  // forward: splits of the key axis; packed: the G heads of a key head share a tile;
+                            // few: packed, at most 32 rows, repeated in the tile's four lane quarters
+  int parts;                // partial results per row: splits, four times as many with `few`
+  float* part_o;            // [B, H, Nq, parts, d]
+  float* part_lse;          // [B, H, Nq, parts]
   float* row_lse;           // backward: [B, H, 128 nqb]; fp32: LSE, +inf where a row sees nothing; bf16: -log2(e) of it
   float* row_d;             // backward: [B, H, 128 nqb]; fp32: D; bf16: -D
   int2* row_span;           // backward, bf16: [B, 128 nqb] the rows' intervals, padded to whole tiles
@@ -114,7 +116,7 @@ int launch_score_fwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_score_bwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 // score_fwd.cu (bf16, tcgen05)
 bool score_packs(int G, int Nq, bool mask, bool table);
-int score_splits(int B, int heads, int nq_tiles, int nkb);
+int score_splits(int B, int heads, int nq_tiles, bool few, int nkb);
 int launch_score_bwd_tc(const ScoreArgs& a, int d, cudaStream_t s);   // score_bwd.cu
 int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s);
 // score_plan.cu

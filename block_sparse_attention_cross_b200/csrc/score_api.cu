@@ -111,11 +111,11 @@ int check_score(ScoreArgs& a, int B, int H, int Hkv, int Nq, int Nk, int d, int 
   return CALIBATT_OK;
 }
 
-// Forward workspace: [part_o][part_lse] of `splits` key splits.
+// Forward workspace: [part_o][part_lse].
 size_t fwd_layout(ScoreArgs& a, int d, void* ws) {
-  if (a.splits <= 1) return 0;
+  if (a.parts <= 1) return 0;
   char* p = static_cast<char*>(ws);
-  const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq * a.splits;
+  const size_t rows = static_cast<size_t>(a.B) * a.H * a.Nq * a.parts;
   a.part_o = reinterpret_cast<float*>(p);
   const size_t off = align256(rows * d * 4);
   a.part_lse = reinterpret_cast<float*>(p + off);
@@ -124,7 +124,9 @@ size_t fwd_layout(ScoreArgs& a, int d, void* ws) {
 
 void fwd_plan(ScoreArgs& a, bool packed) {
   a.packed = packed;
-  a.splits = score_splits(a.B, packed ? a.Hkv : a.H, packed ? 1 : a.nqb, a.nkb);
+  a.few = packed && a.G * a.Nq <= 32;
+  a.splits = score_splits(a.B, packed ? a.Hkv : a.H, packed ? 1 : a.nqb, a.few != 0, a.nkb);
+  a.parts = a.few ? 4 * a.splits : a.splits;
 }
 
 // Backward workspace: [row_lse][row_d][row_span][part_table], 256-byte aligned pieces.

@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const ScoreBias bias{slope, static_cast<float>(j - p0 - half * 64),
                              k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
                              near ? (window ? 0.f : wr[0]) : far};
-        score_columns<F, -1, true, true>(a, terms, r, pf, bias, edge);
+        score_columns<F, -1, true, true>(a, terms, r, pf, bias, edge ? kExact : kByScore);
         if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[t & 1]);
       } else {
 #pragma unroll
@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const ScoreBias bias{slope, static_cast<float>(k0 + half * 64 - p0 - row),
                              k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
                              near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo};
-        score_columns<F, 1, false, true>(a, terms, r, none, bias, edge);
+        score_columns<F, 1, false, true>(a, terms, r, none, bias, edge ? kExact : kByScore);
         if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[wt & 1]);
       }
       if (edge) {
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const ScoreBias bias{slope, static_cast<float>(k0 + half * 64 - p0 - row),
                              k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
                              near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo};
-        score_columns<F, 1, true, true>(a, terms, r, f, bias, edge);
+        score_columns<F, 1, true, true>(a, terms, r, f, bias, edge ? kExact : kByScore);
       } else {
 #pragma unroll
         for (int x = 0; x < 64; ++x) f[x] = 1.f;

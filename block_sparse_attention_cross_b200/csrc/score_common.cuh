@@ -222,7 +222,7 @@ __device__ __forceinline__ void fill_window(const ScoreArgs& a, int h0, int head
 // elsewhere cap - 2 cap / (1 + e^(2x)), two MUFU operations a score, right at
 // both ends.  Both stay within 3e-7 of the cap.  The polynomial leaves the
 // MUFU, which bounds the softmax, to the exponentials.  A row chooses by its
-// own scores, and where the mask cuts it (`exact`) always takes the second
+// own scores, and where the mask cuts it (kExact) always takes the second
 // form, so no other row and no masked place changes a bit of it.
 struct ScoreTerms {
   float sc;                  // scale log2e
@@ -312,17 +312,20 @@ __device__ __forceinline__ void cap_mufu(const ScoreTerms& t, uint32_t (&r)[N], 
 }
 
 // The score function.  DIR = 1: the columns are keys; DIR = -1: queries.
-// BENT: the distance may pass 0 inside the tile; exact: see above.
+// BENT: the distance may pass 0 inside the tile.  form: the cap's, by the row's
+// scores (kByScore), the second (kExact) or the polynomial (kAny: rows whose
+// result nobody reads, which must not drag their warp through both).
+enum CapForm { kByScore, kExact, kAny };
 template <int F, int DIR, bool FACTOR, bool BENT, int N>
 __device__ __forceinline__ void score_columns(const ScoreArgs& a, const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N],
-                                              const ScoreBias& b, bool exact) {
+                                              const ScoreBias& b, int form) {
   // The constant part of the biases: the flat table value, and the distance
   // of column 0 where the distance is linear over the tile.
   const bool slopes = (F & kBias) && a.slopes != nullptr, linear = slopes && (!BENT || b.side != 0);
   const float sl = b.side > 0 ? -b.slope : b.slope;   // -slope |off0 + DIR x| = sl (off0 + DIR x)
   const float shift = F & kBias ? (b.window ? 0.f : b.flat) + (linear ? sl * b.off0 : 0.f) : 0.f;
   if (F & kCap) {
-    if (!exact && score_extent(r) <= t.small) cap_polynomial<FACTOR>(t, r, f, shift);
+    if (form == kAny || (form == kByScore && score_extent(r) <= t.small)) cap_polynomial<FACTOR>(t, r, f, shift);
     else cap_mufu<FACTOR>(t, r, f, shift);
   } else {
     const uint64_t sc = f2pack(t.sc, t.sc), shift2 = f2pack(shift, shift);

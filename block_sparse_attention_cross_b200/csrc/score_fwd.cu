@@ -19,8 +19,11 @@
 //    and rows past a length read as zero;
 //  - the G query heads of a key head share one tile when their rows fit (few
 //    queries: rows g Nq + i), so K and V are read once for all of them;
+//  - with at most 32 such rows they are repeated in all four lane quarters of
+//    the tile, and each warp takes a quarter of every key tile's columns (a
+//    warp reaches only its own TMEM lanes), leaving four partial results;
 //  - few tiles against many keys are split along the keys; k_score_join adds
-//    the splits' results in a fixed order.
+//    the partial results in a fixed order.
 // Bound: MUFU and tensor core together for long queries (see the figures at
 // the launch), HBM for few queries.
 #include <algorithm>
@@ -248,17 +251,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const uint64_t pol = l2_policy_evict_last(), pol_q = l2_policy_evict_first();
     uint8_t* ring = smem + L::OFF_RING + s * R * L::TBYTES;
-    const uint32_t q_bytes = a.packed ? static_cast<uint32_t>(a.G * a.Nq * D * 2) : L::TBYTES;
+    const int copies = a.few ? 4 : 1;
+    const uint32_t q_bytes = a.packed ? static_cast<uint32_t>(copies * a.G * a.Nq * D * 2) : L::TBYTES;
     while (ok && !cu.done) {
       const Walk& w = cu.w;
       if (cu.first) {
         ok = __all_sync(0xffffffffu, mbar_wait(&c->q_empty[s], (qf & 1) ^ 1, &c->abort, a.spin_ns));
         if (!ok) break;
         mbar_arrive_expect_tx_w(&c->q_full[s], q_bytes);
+        for (int r = 0; r < copies; ++r)
 #pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-          tma_load_4d_w(smem + L::OFF_Q + s * L::TBYTES + x * L::BOX, &tmQ, x * 64, w.qb * TILE,
-                        a.packed ? w.hx * a.G : w.hx, w.b, &c->q_full[s], pol_q);
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_4d_w(smem + L::OFF_Q + s * L::TBYTES + x * L::BOX + r * 32 * 128, &tmQ, x * 64, w.qb * TILE,
+                          a.packed ? w.hx * a.G : w.hx, w.b, &c->q_full[s], pol_q);
         ++qf;
       }
       const int hk = a.packed ? w.hx : w.hx / a.G;
@@ -438,8 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int h, i;
       bool live;
       if (a.packed) {
-        const int g = row / a.Nq;
-        i = row - g * a.Nq;
+        const int r = a.few ? lane : row, g = r / a.Nq;
+        i = r - g * a.Nq;
         live = g < a.G;
         h = w.hx * a.G + min(g, a.G - 1);
       } else {
@@ -449,10 +454,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const size_t orow = (static_cast<size_t>(w.b) * a.H + h) * a.Nq + i;   // of lse and the partial results
       __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(a.o.p) + w.b * a.o.sb + h * a.o.sh + i * a.o.sn;
+      const size_t part = orow * a.parts + (a.few ? w.sp * 4 + w4 : w.sp);
       if (!any) {
         if (live) {
-          if (a.splits > 1) {
-            a.part_lse[orow * a.splits + w.sp] = -INFINITY;
+          if (a.parts > 1) {
+            a.part_lse[part] = -INFINITY;
           } else {
             const uint4 z = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -527,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ScoreBias bias = {};
         if (F & kBias) {
           bias.wr = reinterpret_cast<const float*>(smem + L::OFF_WIN + slot * L::WIN + (gb & 1) * (L::WIN / 2)) +
-                    (a.packed ? min(row / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
+                    (a.packed ? min((a.few ? lane : row) / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
           bias.window = near && c->win_info[slot][gb & 1].cuts > 0;
           bias.flat = near ? (bias.window ? 0.f : bias.wr[0]) : k0 > p1 ? far_hi : far_lo;
           bias.side = k0 >= p1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0;
@@ -537,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescale = false;
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
+        const int ch0 = a.few ? w4 : 0, ch1 = a.few ? w4 + 1 : 4;   // this warp's chunks
         auto softmax = [&](auto cut_c) {
           constexpr bool CUT = decltype(cut_c)::value != 0;
           uint32_t r[32];
@@ -555,7 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               at.off0 += static_cast<float>(32 * ch);
               at.wr += 32 * ch;
               float none[32];
-              score_columns<F & 3, 1, false, CUT>(a, terms, r, none, at, CUT && ~bits != 0);
+              score_columns<F & 3, 1, false, CUT>(a, terms, r, none, at,
+                                                 !live ? kAny : CUT && ~bits != 0 ? kExact : kByScore);
             }
             if (CUT) keep_bits(r, bits, -INFINITY);
             return true;
@@ -564,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // First pass: (transformed) scores and the tile's maximum.
             float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
+            for (int ch = ch0; ch < ch1; ++ch) {
               load(ch);
               if (!transform(ch)) {
                 dead |= 1u << ch;
@@ -575,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx0 = fmax3(mx0, u2f(r[x]), u2f(r[x + 1]));
                 mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
               }
-              if (F != 0 || CUT) tmem_st32(t_s + ch * 32, r);
+              if ((F != 0 || CUT) && !a.few) tmem_st32(t_s + ch * 32, r);   // one chunk stays in registers
             }
             const float bmax = fmaxf(mx0, mx1);
             best = fmaxf(best, bmax);
@@ -593,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = m_cand;
               }
             }
-            if (F != 0 || CUT) tmem_st_wait();
+            if ((F != 0 || CUT) && !a.few) tmem_st_wait();
           }
           // Second pass: probabilities, stored as bf16 pairs over the scores
           // already read, and their fp32 sum.
@@ -601,11 +609,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t negm = f2pack(neg, neg);
           float pm0 = 0.f, pm1 = 0.f;
 #pragma unroll 1
-          for (int ch = 0; ch < 4; ++ch) {
+          for (int ch = ch0; ch < ch1; ++ch) {
             uint32_t pk[16];
             bool some = true;
             if (!CUT || !((dead >> ch) & 1u)) {
-              load(ch);
+              if ((F & kBounded) || !a.few) load(ch);
               if (F & kBounded) some = transform(ch);
             } else {
               some = false;
@@ -638,6 +646,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) softmax(IntC<1>{});
         else softmax(IntC<0>{});
         if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[slot][gb & 1]);
+        if (a.few) {   // the other warps' columns are 0 in these lanes
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) pk[x] = 0;
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch)
+            if (ch != w4) tmem_st16(t_s + ch * 16, pk);
+        }
         if (rescale) {
 #pragma unroll 1
           for (int q4 = 0; q4 < D / 32; ++q4) {
@@ -676,8 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       see_bad(gb);
       const float inv_l = row_bad ? NAN : l == 0.f ? 0.f : 1.f / (l + corr);
       const float row_lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-      if (a.splits > 1) {
-        float* po = a.part_o + (orow * a.splits + w.sp) * D;
+      if (a.parts > 1) {
+        float* po = a.part_o + part * D;
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
           uint32_t ro[32];
@@ -692,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                               u2f(ro[4 * x + 3]) * inv_l);
           }
         }
-        if (live) a.part_lse[orow * a.splits + w.sp] = row_lse;
+        if (live) a.part_lse[part] = row_lse;
       } else {
 #pragma unroll 1
         for (int q4 = 0; q4 < D / 32; ++q4) {
@@ -728,45 +744,57 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the splits of a row: weights 2^(lse_s - max), in split order.  One
-// warp a row, a lane D / 32 columns; reads the partial results once.
+// Joins the partial results of a row: weights e^(lse_s - max).  One CTA a row;
+// warp w adds up the parts w, w + 4, ... (a lane D / 32 columns), then the
+// warps' sums are added in warp order: a fixed order.  Reads the partial
+// results once.
 template <int D>
 __global__ void __launch_bounds__(128) k_score_join(const ScoreArgs a) {
-  const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
-  const long long r = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (r >= rows) return;
-  const int lane = threadIdx.x & 31;
-  const float* pl = a.part_lse + r * a.splits;
+  constexpr int C = D / 32;
+  __shared__ float sums[4][D], norm[4];
+  const long long r = blockIdx.x;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const float* pl = a.part_lse + r * a.parts;
   float mx = -INFINITY;
-  bool nan = false;
-  for (int s = lane; s < a.splits; s += 32) {
-    mx = fmaxf(mx, pl[s]);
-    nan |= isnan(pl[s]);
-  }
+  for (int s = lane; s < a.parts; s += 32) mx = fmaxf(mx, pl[s]);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-  nan = __any_sync(0xffffffffu, nan);
-  float acc[D / 32] = {}, l = 0.f;
-  if (mx != -INFINITY) {
-    for (int s = 0; s < a.splits; ++s) {
-      const float x = pl[s];
-      if (x == -INFINITY) continue;   // its partial O was not written
-      const float wgt = expf(x - mx);
-      l += wgt;
-      const float* po = a.part_o + (r * a.splits + s) * D + lane * (D / 32);
+  float acc[C] = {}, l = 0.f;
+  // eight parts' loads in flight; a part that saw nothing has no partial O
+  for (int s0 = w; s0 < a.parts; s0 += 32) {
+    float x[8], po[8][C];
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) acc[e] = fmaf(wgt, po[e], acc[e]);
+    for (int k = 0; k < 8; ++k) {
+      const int s = min(s0 + 4 * k, a.parts - 1);
+      x[k] = s0 + 4 * k < a.parts ? pl[s] : -INFINITY;
+#pragma unroll
+      for (int e = 0; e < C; ++e) po[k][e] = a.part_o[(r * a.parts + s) * D + lane * C + e];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (x[k] == -INFINITY) continue;
+      const float wgt = expf(x[k] - mx);   // NaN stays NaN
+      l += wgt;
+#pragma unroll
+      for (int e = 0; e < C; ++e) acc[e] = fmaf(wgt, po[k][e], acc[e]);
     }
   }
+#pragma unroll
+  for (int e = 0; e < C; ++e) sums[w][lane * C + e] = acc[e];
+  if (lane == 0) norm[w] = l;
+  __syncthreads();
+  l = (norm[0] + norm[1]) + (norm[2] + norm[3]);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int i = static_cast<int>(r % a.Nq);
   const int bh = static_cast<int>(r / a.Nq), b = bh / a.H, h = bh % a.H;
-  __nv_bfloat16* op =
-      reinterpret_cast<__nv_bfloat16*>(a.o.p) + b * a.o.sb + h * a.o.sh + i * a.o.sn + lane * (D / 32);
-#pragma unroll
-  for (int e = 0; e < D / 32; e += 2)
-    *reinterpret_cast<uint32_t*>(op + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0 && a.lse != nullptr) a.lse[r] = nan ? NAN : l == 0.f ? -INFINITY : mx + logf(l);
+  __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(a.o.p) + b * a.o.sb + h * a.o.sh + i * a.o.sn;
+  if (threadIdx.x < D / 2) {
+    const int e = threadIdx.x * 2;
+    const float x = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
+    const float y = (sums[0][e + 1] + sums[1][e + 1]) + (sums[2][e + 1] + sums[3][e + 1]);
+    *reinterpret_cast<uint32_t*>(op + e) = pack_bf16x2(x * inv, y * inv);
+  }
+  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[r] = l == 0.f ? -INFINITY : mx + logf(l);
 }
 
 template <int D, int F>
@@ -796,9 +824,9 @@ int launch(const ScoreArgs& a, int sms, cudaStream_t s) {
   kern<<<grid, kThreads, Layout<D>::SMEM, s>>>(tq, tk, tv, f);
   count_launch();
   if ((rc = check_launch("k_score_fwd"))) return rc;
-  if (a.splits > 1) {
+  if (a.parts > 1) {
     const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
-    k_score_join<D><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(a);
+    k_score_join<D><<<static_cast<unsigned>(rows), 128, 0, s>>>(a);
     count_launch();
     return check_launch("k_score_join");
   }
@@ -810,16 +838,19 @@ int launch(const ScoreArgs& a, int sms, cudaStream_t s) {
 // Whether the G query heads of a key head share a tile: their rows fit, no
 // mask (it may differ between the heads) and the table's windows fit.
 bool score_packs(int G, int Nq, bool mask, bool table) {
-  return G > 1 && static_cast<long long>(G) * Nq <= TILE && !mask && (!table || G <= kMaxPackedTable);
+  return static_cast<long long>(G) * Nq <= TILE && !mask && (!table || G <= kMaxPackedTable);
 }
 
-// Splits of the key axis.  296 slots (two on each of 148 SMs) want a tile
-// each; with fewer tiles than slots the keys are divided, but a split keeps
-// at least 4 key tiles.
-int score_splits(int B, int heads, int nq_tiles, int nkb) {
+// Splits of the key axis, for 296 slots (two on each of 148 SMs) of one unit
+// (query tile and split) at a time.  Units of equal length fill whole rounds
+// of the slots when there are floor(296 rounds / tiles) splits of each tile.
+// Tiles of few rows (serving) write little per split and their sequences
+// differ in length, so they take four rounds of at least four key tiles a
+// split; full tiles write 512 bytes of partial sums per row and split, so they
+// are split into one round, and only when they leave half of the slots idle.
+int score_splits(int B, int heads, int nq_tiles, bool few, int nkb) {
   const long long tiles = static_cast<long long>(B) * heads * nq_tiles;
-  if (tiles >= 296) return 1;
-  const long long want = (296 + tiles - 1) / tiles;
+  const long long want = (few ? 4 : 1) * 296 / tiles;
   return static_cast<int>(std::max<long long>(1, std::min<long long>(want, nkb / 4)));
 }
 

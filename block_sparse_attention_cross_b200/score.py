@@ -12,6 +12,7 @@ marshals arguments, allocates outputs and workspace and passes the stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 from dataclasses import dataclass
 
@@ -25,11 +26,20 @@ _DTYPES = {torch.bfloat16: BF16, torch.float32: FP32}
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # torch.cuda.current_stream builds a Stream object around this number (3 us a call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _on_device(device, call):
+    """Runs ``call`` with ``device`` current (the usual case, that it is already, costs no context manager)."""
+    if torch.cuda.current_device() == device.index:
+        return call()
+    with torch.cuda.device(device):
+        return call()
 
 
 @dataclass
@@ -104,10 +114,9 @@ def attn_spans(B, Nq, Nk, *, causal=False, docs=None, prefix=None, kv_len=None, 
     sp = AttnSpans(B, Nq, Nk, torch.empty((B, Nq, 2), dtype=torch.int32, device=device),
                    torch.empty((B, -(-Nq // 128), 4), dtype=torch.int32, device=device),
                    torch.empty(B, dtype=torch.int32, device=device))
-    with torch.cuda.device(device):
-        check(load().calibatt_attn_spans(B, Nq, Nk, int(bool(causal)), _ptr(docs), n_docs, _ptr(prefix), _ptr(kv_len),
-                                         _ptr(q_len), _ptr(q_start), _ptr(sp.row), _ptr(sp.tile), _ptr(sp.q_start),
-                                         _stream(device)))
+    check(_on_device(device, lambda: load().calibatt_attn_spans(
+        B, Nq, Nk, int(bool(causal)), _ptr(docs), n_docs, _ptr(prefix), _ptr(kv_len), _ptr(q_len), _ptr(q_start),
+        _ptr(sp.row), _ptr(sp.tile), _ptr(sp.q_start), _stream(device))))
     return sp
 
 
@@ -123,22 +132,24 @@ def relative_buckets(n_buckets, max_distance, bidirectional=True, device="cuda")
 
 def _tensor4(name, t, shape, dtype, device):
     """Checks a [B, heads, N, d] tensor and returns its ``calibatt_tensor4``."""
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    st = t.stride()
-    if st[3] != 1 or any(n > 1 and (s <= 0 or s * t.element_size() % 16) for n, s in zip(shape[:3], st[:3])):
+    sb, sh, sn, sd = t.stride()
+    step = 16 // t.element_size()
+    if (sd != 1 or (shape[0] > 1 and (sb <= 0 or sb % step)) or (shape[1] > 1 and (sh <= 0 or sh % step))
+            or (shape[2] > 1 and (sn <= 0 or sn % step))):
         raise ValueError(f"{name}: the last dimension must be contiguous and the others' strides positive multiples "
-                         f"of 16 bytes, got strides {st} (an expanded tensor needs .contiguous())")
-    return _lib.Tensor4(t.data_ptr(), st[0], st[1], st[2])
+                         f"of 16 bytes, got strides {t.stride()} (an expanded tensor needs .contiguous())")
+    return _lib.Tensor4(t.data_ptr(), sb, sh, sn)
 
 
 def _flat(name, t, shape, dtype, device):
     """Checks a contiguous operand (None: not given)."""
     if t is None:
         return
-    if tuple(t.shape) != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
     if not t.is_cuda or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
@@ -188,6 +199,20 @@ def _prepare(q, k, v, spans, scale, cap, slopes, table, buckets, mask, map_offse
     return (B, H, Hkv, Nq, Nk, d), sc
 
 
+@functools.lru_cache(maxsize=1024)
+def _fwd_bytes(*sizes):
+    n = ctypes.c_size_t(0)
+    check(load().calibatt_score_attn_fwd_workspace_size(*sizes, ctypes.byref(n)))
+    return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _bwd_bytes(*sizes):
+    n = ctypes.c_size_t(0)
+    check(load().calibatt_score_attn_bwd_workspace_size(*sizes, ctypes.byref(n)))
+    return n.value
+
+
 def _workspace(nbytes, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
@@ -218,15 +243,14 @@ def score_attn_fwd(q, k, v, spans: AttnSpans, *, scale=None, cap=0.0, slopes=Non
     if return_lse and lse is None:
         lse = torch.empty((B, H, Nq), device=dev, dtype=torch.float32)
     _flat("lse", lse, (B, H, Nq), torch.float32, dev)
-    n = ctypes.c_size_t(0)
     sizes = (B, H, Hkv, Nq, Nk, d, _DTYPES[dt])
-    check(load().calibatt_score_attn_fwd_workspace_size(*sizes, ctypes.byref(n)))
+    nbytes = _fwd_bytes(*sizes)
+    ws = _workspace(nbytes, dev)
+    ref = ctypes.byref
     sp = spans.as_struct()
-    with torch.cuda.device(dev):
-        ws = _workspace(n.value, dev)
-        check(load().calibatt_score_attn_fwd(ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), ctypes.byref(to),
-                                             _ptr(lse), *sizes, ctypes.byref(sp), ctypes.byref(sc), _ptr(ws), n.value,
-                                             _ptr(status), _stream(dev)))
+    check(_on_device(dev, lambda: load().calibatt_score_attn_fwd(
+        ref(tq), ref(tk), ref(tv), ref(to), _ptr(lse), *sizes, ref(sp), ref(sc), _ptr(ws), nbytes, _ptr(status),
+        _stream(dev))))
     return (out, lse) if return_lse else out
 
 
@@ -250,14 +274,12 @@ def score_attn_bwd(dout, q, k, v, o, lse, spans: AttnSpans, *, scale=None, cap=0
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     outs = [_tensor4("dq", dq, qs, dt, dev), _tensor4("dk", dk, ks, dt, dev), _tensor4("dv", dv, ks, dt, dev)]
     dtable = None if table is None else torch.empty_like(table)
-    n = ctypes.c_size_t(0)
     sizes = (B, H, Hkv, Nq, Nk, d, _DTYPES[dt])
-    check(load().calibatt_score_attn_bwd_workspace_size(*sizes, 0 if table is None else table.shape[1],
-                                                        ctypes.byref(n)))
+    nbytes = _bwd_bytes(*sizes, 0 if table is None else table.shape[1])
+    ws = _workspace(nbytes, dev)
+    ref = ctypes.byref
     sp = spans.as_struct()
-    with torch.cuda.device(dev):
-        ws = _workspace(n.value, dev)
-        check(load().calibatt_score_attn_bwd(*(ctypes.byref(t) for t in ins), _ptr(lse),
-                                             *(ctypes.byref(t) for t in outs), _ptr(dtable), *sizes, ctypes.byref(sp),
-                                             ctypes.byref(sc), _ptr(ws), n.value, _ptr(status), _stream(dev)))
+    check(_on_device(dev, lambda: load().calibatt_score_attn_bwd(
+        *map(ref, ins), _ptr(lse), *map(ref, outs), _ptr(dtable), *sizes, ref(sp), ref(sc), _ptr(ws), nbytes,
+        _ptr(status), _stream(dev))))
     return (dq, dk, dv) if table is None else (dq, dk, dv, dtable)
