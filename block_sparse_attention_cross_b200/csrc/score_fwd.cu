@@ -167,6 +167,9 @@ __device__ __forceinline__ void cursor_next(const FwdArgs& f, Cursor& c) {
 // Beside the ScoreForm bits: capped scores without a bias and with a cap of
 // at most kBoundedCap need no maximum.
 constexpr int kBounded = 4;
+// At most 32 rows, repeated in the four lane quarters (a kernel of its own, so
+// that neither form carries the other's code).
+constexpr int kFew = 8;
 // Largest cap in log2 units that goes without a maximum: probabilities
 // 2^score lie in 2^+-80, their sums over 2^24 keys and their products with V
 // (|v| < 2^20) inside fp32, and bf16 has fp32's exponents.
@@ -199,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_score_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ FwdArgs f) {
   using L = Layout<D>;
+  constexpr bool FEW = (F & kFew) != 0;
   constexpr int R = L::RING;
   static_assert(sizeof(Ctrl<R>) <= L::CTRL, "control block");
   const ScoreArgs& a = f.a;
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     const uint64_t pol = l2_policy_evict_last(), pol_q = l2_policy_evict_first();
     uint8_t* ring = smem + L::OFF_RING + s * R * L::TBYTES;
-    const int copies = a.few ? 4 : 1;
+    const int copies = FEW ? 4 : 1;
     const uint32_t q_bytes = a.packed ? static_cast<uint32_t>(copies * a.G * a.Nq * D * 2) : L::TBYTES;
     while (ok && !cu.done) {
       const Walk& w = cu.w;
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = t_s + 128;
     // Scores are in log2 units.
     const ScoreTerms terms = score_terms(a);
-    const float c2 = F == 0 ? terms.sc : 1.f;   // plain scores: the scale is folded into the exponent
+    const float c2 = (F & 3) == 0 ? terms.sc : 1.f;   // plain scores: the scale is folded into the exponent
     const uint64_t c2x2 = f2pack(c2, c2);
     uint32_t gb = 0;
     int tiles = 0;
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int h, i;
       bool live;
       if (a.packed) {
-        const int r = a.few ? lane : row, g = r / a.Nq;
+        const int r = FEW ? lane : row, g = r / a.Nq;
         i = r - g * a.Nq;
         live = g < a.G;
         h = w.hx * a.G + min(g, a.G - 1);
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const size_t orow = (static_cast<size_t>(w.b) * a.H + h) * a.Nq + i;   // of lse and the partial results
       __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(a.o.p) + w.b * a.o.sb + h * a.o.sh + i * a.o.sn;
-      const size_t part = orow * a.parts + (a.few ? w.sp * 4 + w4 : w.sp);
+      const size_t part = orow * a.parts + (FEW ? w.sp * 4 + w4 : w.sp);
       if (!any) {
         if (live) {
           if (a.parts > 1) {
@@ -533,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ScoreBias bias = {};
         if (F & kBias) {
           bias.wr = reinterpret_cast<const float*>(smem + L::OFF_WIN + slot * L::WIN + (gb & 1) * (L::WIN / 2)) +
-                    (a.packed ? min((a.few ? lane : row) / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
+                    (a.packed ? min((FEW ? lane : row) / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
           bias.window = near && c->win_info[slot][gb & 1].cuts > 0;
           bias.flat = near ? (bias.window ? 0.f : bias.wr[0]) : k0 > p1 ? far_hi : far_lo;
           bias.side = k0 >= p1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0;
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescale = false;
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-        const int ch0 = a.few ? w4 : 0, ch1 = a.few ? w4 + 1 : 4;   // this warp's chunks
+        const int ch0 = FEW ? w4 : 0, ch1 = FEW ? w4 + 1 : 4;   // this warp's chunks
         auto softmax = [&](auto cut_c) {
           constexpr bool CUT = decltype(cut_c)::value != 0;
           uint32_t r[32];
@@ -557,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto transform = [&](int ch) {
             const uint32_t bits = CUT ? bits_below(e1 - 32 * ch) & ~bits_below(e0 - 32 * ch) : 0xffffffffu;
             if (CUT && !__any_sync(0xffffffffu, bits != 0)) return false;
-            if (F != 0) {
+            if ((F & 3) != 0) {
               ScoreBias at = bias;
               at.off0 += static_cast<float>(32 * ch);
               at.wr += 32 * ch;
@@ -583,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mx0 = fmax3(mx0, u2f(r[x]), u2f(r[x + 1]));
                 mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
               }
-              if ((F != 0 || CUT) && !a.few) tmem_st32(t_s + ch * 32, r);   // one chunk stays in registers
+              if (((F & 3) != 0 || CUT) && !FEW) tmem_st32(t_s + ch * 32, r);   // one chunk stays in registers
             }
             const float bmax = fmaxf(mx0, mx1);
             best = fmaxf(best, bmax);
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = m_cand;
               }
             }
-            if ((F != 0 || CUT) && !a.few) tmem_st_wait();
+            if (((F & 3) != 0 || CUT) && !FEW) tmem_st_wait();
           }
           // Second pass: probabilities, stored as bf16 pairs over the scores
           // already read, and their fp32 sum.
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t pk[16];
             bool some = true;
             if (!CUT || !((dead >> ch) & 1u)) {
-              if ((F & kBounded) || !a.few) load(ch);
+              if ((F & kBounded) || !FEW) load(ch);
               if (F & kBounded) some = transform(ch);
             } else {
               some = false;
@@ -646,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) softmax(IntC<1>{});
         else softmax(IntC<0>{});
         if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[slot][gb & 1]);
-        if (a.few) {   // the other warps' columns are 0 in these lanes
+        if (FEW) {   // the other warps' columns are 0 in these lanes
           uint32_t pk[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) pk[x] = 0;
@@ -860,12 +864,17 @@ int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s) {
   const bool bias = a.slopes != nullptr || a.table != nullptr;
   const int form = (a.cap > 0.f ? kCap : 0) | (bias ? kBias : 0) |
                    (a.cap > 0.f && !bias && a.cap * kLog2e <= kBoundedCap ? kBounded : 0);
+  auto go = [&](auto form_c) {
+    constexpr int F = decltype(form_c)::value;
+    if (a.few) return d == 128 ? launch<128, F | kFew>(a, sms, s) : launch<64, F | kFew>(a, sms, s);
+    return d == 128 ? launch<128, F>(a, sms, s) : launch<64, F>(a, sms, s);
+  };
   switch (form) {
-    case 0: return d == 128 ? launch<128, 0>(a, sms, s) : launch<64, 0>(a, sms, s);
-    case kCap: return d == 128 ? launch<128, kCap>(a, sms, s) : launch<64, kCap>(a, sms, s);
-    case kCap | kBounded: return d == 128 ? launch<128, kCap | kBounded>(a, sms, s) : launch<64, kCap | kBounded>(a, sms, s);
-    case kBias: return d == 128 ? launch<128, kBias>(a, sms, s) : launch<64, kBias>(a, sms, s);
-    default: return d == 128 ? launch<128, kCap | kBias>(a, sms, s) : launch<64, kCap | kBias>(a, sms, s);
+    case 0: return go(IntC<0>{});
+    case kCap: return go(IntC<kCap>{});
+    case kCap | kBounded: return go(IntC<kCap | kBounded>{});
+    case kBias: return go(IntC<kBias>{});
+    default: return go(IntC<kCap | kBias>{});
   }
 }
 
