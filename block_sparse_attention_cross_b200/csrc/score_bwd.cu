@@ -40,6 +40,8 @@ constexpr uint32_t kSoftmaxRegs = 208;
 constexpr uint32_t kControlRegs = 88;
 static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchRegs, "register split");
 constexpr int kProducer = 8, kMma = 9, kWindow = 10;
+// Beside the ScoreForm bits: the dQ kernel sums the table's gradient.
+constexpr int kGrad = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kCtrlBytes = 2048;              // barriers and small state, checked against its size below
 constexpr uint32_t kRowBytes = 512 + 512 + 1024;   // -LSE, -D and interval of a tile's rows
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_w(&c->drain);
     mbar_wait(&c->drain, 0, nullptr, a.spin_ns);
   } else if (warp == kWindow) {
-    if (((F & kBias) && a.table != nullptr)) {
+    if ((F & kBias) && a.table != nullptr) {
       QueryWalk w;
       bool bad = false, ok = true;
       uint32_t t = 0;
@@ -363,8 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float4* nlse = reinterpret_cast<const float4*>(rows) + half * 16;
       const float4* nd = reinterpret_cast<const float4*>(rows + 512) + half * 16;
       float slope = 0.f, far = 0.f;
-      if (((F & kBias) && a.slopes != nullptr)) slope = a.slopes[h] * kLog2e;
-      if (((F & kBias) && a.table != nullptr) && !near) {
+      if ((F & kBias) && a.slopes != nullptr) slope = a.slopes[h] * kLog2e;
+      if ((F & kBias) && a.table != nullptr && !near) {
         bool bad = false;
         const int n = score_bucket(a, k0 > p0 ? a.R : -a.R, &bad);
         far = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n]) * kLog2e;
@@ -372,105 +374,124 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bool got = mbar_wait(&c->s_full, t & 1, &c->abort, a.spin_ns) &&
                  mbar_wait(&c->ring_full[e], (t / R) & 1, &c->abort, a.spin_ns);
-      if (got && ((F & kBias) && a.table != nullptr)) got = mbar_wait(&c->win_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && (F & kBias) && a.table != nullptr) got = mbar_wait(&c->win_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
       if (got && edge) got = mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
-      uint32_t r[64];
-      tmem_ld32(tSh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-      tmem_ld32(tSh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-      tmem_ld_wait();
-      reg_fence(r);
-      uint32_t seen0 = 0xffffffffu, seen1 = 0xffffffffu;
-      if (edge) {
-        const int4* span = reinterpret_cast<const int4*>(rows + 1024) + half * 32;
-        seen0 = seen1 = 0;
-#pragma unroll
-        for (int x = 0; x < 64; x += 2) {
-          const int4 v = span[x / 2];
-          const uint32_t bits = (j >= v.x && j < v.y ? 1u : 0u) | (j >= v.z && j < v.w ? 2u : 0u);
-          if (x < 32) seen0 |= bits << x; else seen1 |= bits << (x - 32);
-        }
+      // column x: query 64 half + x, offset j - p falls with x
+      ScoreBias bias = {};
+      if (F & kBias) {
+        bias.wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (t & 1) * 256 + row + TILE - 1 - half * 64;
+        bias.window = near && c->win_info[t & 1].cuts > 0;
+        bias.flat = near ? (bias.window ? 0.f : bias.wr[0]) : far;
+        bias.side = k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0;
+        bias.slope = slope;
+        bias.off0 = static_cast<float>(j - p0 - half * 64);
       }
-      float pf[64];   // first the cap's factor, then P times it
-      if (xform) {
-        // column x: query 64 half + x, offset j - p falls with x
-        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (t & 1) * 256 + row + TILE - 1 - half * 64;
-        const bool window = near && c->win_info[t & 1].cuts > 0;
-        const ScoreBias bias{slope, static_cast<float>(j - p0 - half * 64),
-                             k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
-                             near ? (window ? 0.f : wr[0]) : far};
-        score_columns<F, -1, true, true>(a, terms, r, pf, bias, edge ? kExact : kByScore);
-        if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[t & 1]);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 64; ++x) pf[x] = 1.f;
-      }
-      if (edge) {
-        // Queries with a NaN or an infinity would leave it in every key's sums
-        // through a probability of 0: their rows of Q (read by S, which is
-        // complete) and of dO (read by dP, awaited above) are zeroed before
-        // the second products.  Keys that are seen get it from P or dS, which
-        // are NaN then.
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x)
-          clean_box_row(smem + (half == 0 ? L::OFF_Q : L::OFF_DO) + e * L::TB + x * L::BOX + row * 128, row);
-        fence_proxy_async_smem();
-      }
-      // P, rounded to bf16 for dV, and P times the cap's factor kept for dS
-      {
-        float pv[64];
-#pragma unroll
-        for (int x = 0; x < 64; x += 4) {
-          const float4 nl = nlse[x / 4];
-          float y0, y1, y2, y3;
-          f2unpack(ffma2(f2pack(u2f(r[x]), u2f(r[x + 1])), c2x2, f2pack(nl.x, nl.y)), y0, y1);
-          f2unpack(ffma2(f2pack(u2f(r[x + 2]), u2f(r[x + 3])), c2x2, f2pack(nl.z, nl.w)), y2, y3);
-          pv[x] = ex2_approx(y0);
-          pv[x + 1] = ex2_approx(y1);
-          pv[x + 2] = ex2_approx(y2);
-          pv[x + 3] = ex2_approx(y3);
+      // A tile that the mask cuts, or where the distance passes 0, has code of
+      // its own: the ordinary tiles are bound by instruction fetch as much as
+      // by arithmetic.
+      auto pair = [&](auto cut_c) {
+        constexpr bool CUT = decltype(cut_c)::value != 0;
+        uint32_t seen0 = 0xffffffffu, seen1 = 0xffffffffu;
+        if (CUT) {
+          const int2* span = reinterpret_cast<const int2*>(rows + 1024) + half * 64;
+          seen0 = seen1 = 0;
+#pragma unroll 4
+          for (int x = 0; x < 32; ++x) {
+            const int2 u = span[x], v = span[x + 32];
+            if (j >= u.x && j < u.y) seen0 |= 1u << x;
+            if (j >= v.x && j < v.y) seen1 |= 1u << x;
+          }
+          // Queries with a NaN or an infinity would leave it in every key's
+          // sums through a probability of 0: their rows of Q (read by S, which
+          // is complete) and of dO (read by dP, awaited above) are zeroed
+          // before the second products.  Keys that are seen get it from P or
+          // dS, which are NaN then.
+          if (edge) clean_row<D / 64>(smem + (half == 0 ? L::OFF_Q : L::OFF_DO) + e * L::TB, row);
         }
-        if (edge) {
-#pragma unroll
-          for (int x = 0; x < 64; ++x)
-            if (!((x < 32 ? seen0 >> x : seen1 >> (x - 32)) & 1u)) pv[x] = 0.f;
+        uint32_t r[64];
+        tmem_ld32(tSh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+        tmem_ld32(tSh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+        tmem_ld_wait();
+        reg_fence(r);
+        float pf[64];   // first the cap's factor, then P times it
+        if (F != 0) {
+          score_columns<F, -1, true, CUT>(a, terms, r, pf, bias, CUT && edge ? kExact : kByScore);
+          if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[t & 1]);
         }
-        store_half(tSh, pv);
+        // P, rounded to bf16 for dV, and P times the cap's factor kept for dS
+#pragma unroll
+        for (int c32 = 0; c32 < 2; ++c32) {
+          const uint32_t seen = c32 ? seen1 : seen0;
+          float pv[32];
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            const float4 nl = nlse[c32 * 8 + x / 4];
+            const int o = c32 * 32 + x;
+            f2unpack(ffma2(pair_of(r, o), c2x2, f2pack(nl.x, nl.y)), pv[x], pv[x + 1]);
+            f2unpack(ffma2(pair_of(r, o + 2), c2x2, f2pack(nl.z, nl.w)), pv[x + 2], pv[x + 3]);
+          }
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            pv[x] = ex2_approx(pv[x]);
+            pv[x + 1] = ex2_approx(pv[x + 1]);
+            if (CUT) {
+              if (!(seen & (1u << x))) pv[x] = 0.f;
+              if (!(seen & (2u << x))) pv[x + 1] = 0.f;
+            }
+            pk[x / 2] = pack_bf16x2(pv[x], pv[x + 1]);
+            const int o = c32 * 32 + x;
+            if (F & kCap) {
+              f2unpack(fmul2(f2pack(pf[o], pf[o + 1]), f2pack(pv[x], pv[x + 1])), pf[o], pf[o + 1]);
+            } else {
+              pf[o] = pv[x];
+              pf[o + 1] = pv[x + 1];
+            }
+          }
+          tmem_st16(tSh + c32 * 16, pk);
+        }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&c->p_full);
+        ok = __all_sync(0xffffffffu, mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns));
+        if (!ok) return;
+        tc_fence_after();
+        tmem_ld32(tPh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
+        tmem_ld32(tPh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
+        tmem_ld_wait();
+        reg_fence(r);
 #pragma unroll
-        for (int x = 0; x < 64; ++x) pf[x] *= pv[x];
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns));
+        for (int c32 = 0; c32 < 2; ++c32) {
+          const uint32_t seen = c32 ? seen1 : seen0;
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            const float4 d4 = nd[c32 * 8 + x / 4];
+            const int o = c32 * 32 + x;
+            float y0, y1, y2, y3;
+            f2unpack(fmul2(fadd2(pair_of(r, o), f2pack(d4.x, d4.y)), f2pack(pf[o], pf[o + 1])), y0, y1);
+            f2unpack(fmul2(fadd2(pair_of(r, o + 2), f2pack(d4.z, d4.w)), f2pack(pf[o + 2], pf[o + 3])), y2, y3);
+            if (CUT) {   // dP of a masked pair may be NaN
+              if (!(seen & (1u << x))) y0 = 0.f;
+              if (!(seen & (2u << x))) y1 = 0.f;
+              if (!(seen & (4u << x))) y2 = 0.f;
+              if (!(seen & (8u << x))) y3 = 0.f;
+            }
+            pk[x / 2] = pack_bf16x2(y0, y1);
+            pk[x / 2 + 1] = pack_bf16x2(y2, y3);
+          }
+          tmem_st16(tPh + c32 * 16, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&c->ds_full);
+      };
+      if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) pair(IntC<1>{});
+      else pair(IntC<0>{});
       if (!ok) break;
-      tc_fence_after();
-      tmem_ld32(tPh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-      tmem_ld32(tPh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-      tmem_ld_wait();
-      reg_fence(r);
-#pragma unroll
-      for (int x = 0; x < 64; x += 4) {
-        const float4 d4 = nd[x / 4];
-        float y0, y1;
-        f2unpack(fmul2(fadd2(f2pack(u2f(r[x]), u2f(r[x + 1])), f2pack(d4.x, d4.y)), f2pack(pf[x], pf[x + 1])), y0, y1);
-        pf[x] = y0;
-        pf[x + 1] = y1;
-        f2unpack(fmul2(fadd2(f2pack(u2f(r[x + 2]), u2f(r[x + 3])), f2pack(d4.z, d4.w)), f2pack(pf[x + 2], pf[x + 3])), y0, y1);
-        pf[x + 2] = y0;
-        pf[x + 3] = y1;
-      }
-      if (edge) {
-#pragma unroll
-        for (int x = 0; x < 64; ++x)
-          if (!((x < 32 ? seen0 >> x : seen1 >> (x - 32)) & 1u)) pf[x] = 0.f;
-      }
-      store_half(tPh, pf);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&c->ds_full);
     }
     // ---- epilogue: warpgroup 0 writes dV, warpgroup 1 dK ---------------------
     const bool live = j < a.Nk;
@@ -521,7 +542,7 @@ template <int RK, int RV>
 struct DqCtrl {
   uint64_t q_full, k_full[RK], k_empty[RK], v_full[RV], v_empty[RV];
   uint64_t a_full[2], a_free[2], mid;   // first sweep
-  uint64_t s_full[2], dp_full, ds_full, o_full, drain;
+  uint64_t s_full[2], dp_full, dp_free, ds_full, o_full, drain;
   uint64_t win_full[2], win_empty[2];
   WindowInfo win_info[2];
   uint32_t tmem_base;
@@ -532,9 +553,71 @@ struct DqCtrl {
 // First sweep: S and dP of key tile t in the column pairs [128 (t & 1), + 128)
 // and [256 + 128 (t & 1), + 128), issued two tiles ahead of the softmax warps.
 // Second sweep: S of key tile t in [128 (t & 1), + 128), dS in place; dP [256, 384);
-// dQ at 384.  Issue order: S(0), dP(0), S(1); then per tile t, once dS(t) is
-// stored, dP(t + 1), dQ(t), S(t + 2): the scores are a tile ahead, so the
-// exponentials of tile t + 1 start at once, and dP(t + 1) arrives during them.
+// dQ at 384.  Issue order: S(0), dP(0), S(1); then per tile t, once dP(t) is
+// read, dP(t + 1), and once dS(t) is stored, dQ(t) and S(t + 2): the scores are
+// a tile ahead and dP(t + 1) is formed during the second half of tile t's
+// arithmetic.
+// Adds the warp's sum of v to *acc, in a fixed order.
+__device__ __forceinline__ void add_to_bucket(float* acc, float v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+  if (lane_id() == 0) *acc += v;
+  __syncwarp();
+}
+
+// dZ of 32 columns whose offsets meet boundaries k ... k1 - 1 of a window:
+// column x is entry `entry` + x.  Per segment the row's sum, added up over the
+// warp.  (Out of line, as the next one: few tiles near the diagonal need them.)
+__device__ __forceinline__ void sum_by_cuts(const uint32_t (&g)[32], const WindowInfo& info, int k, int k1, int entry,
+                                         float* acc) {
+  float before = 0.f;
+  for (; k <= k1; ++k) {
+    const int cut = k < k1 ? info.at[k] - entry : 32;
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      if (x < cut) s0 += u2f(g[x]);
+      if (x + 1 < cut) s1 += u2f(g[x + 1]);
+    }
+    add_to_bucket(acc + info.bucket[k], s0 + s1 - before);
+    before = s0 + s1;
+  }
+}
+
+// dZ of 32 rows and 32 columns summed along the diagonals (one offset each) by
+// passing a running sum from row to row: after column x lane 31 holds the sum
+// of the diagonal that ends in it, with bucket b[x]; 31 more steps drain the
+// others.  Runs of offsets of one bucket are added up before the accumulators
+// are touched.
+__device__ __forceinline__ void sum_by_diagonals(const uint32_t (&g)[32], const uint8_t* b, float* acc) {
+  const int lane = lane_id();
+  float diag = 0.f, run = 0.f;
+  int cur = b[0];
+  auto add = [&](int x) {
+    const int n = b[x];
+    if (n != cur) {
+      if (lane == 31) acc[cur] += run;
+      run = 0.f;
+      cur = n;
+    }
+    run += diag;
+  };
+#pragma unroll
+  for (int x = 0; x < 32; ++x) {
+    const float up = __shfl_up_sync(0xffffffffu, diag, 1);
+    diag = u2f(g[x]) + (lane == 0 ? 0.f : up);
+    add(x);
+  }
+#pragma unroll 1
+  for (int x = 32; x < 63; ++x) {
+    const float up = __shfl_up_sync(0xffffffffu, diag, 1);
+    diag = lane == 0 ? 0.f : up;
+    add(x);
+  }
+  if (lane == 31) acc[cur] += run;
+  __syncwarp();
+}
+
 template <int D, int F>
 __global__ void __launch_bounds__(kThreads, 1)
     k_score_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -575,6 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&c->mid, 256);
     mbar_init(&c->dp_full, 1);
+    mbar_init(&c->dp_free, 256);
     mbar_init(&c->ds_full, 256);
     mbar_init(&c->o_full, 1);
     mbar_init(&c->drain, 1);
@@ -585,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tmV);
     tma_prefetch_desc(&tmDO);
   }
-  if (((F & kBias) && a.dtable != nullptr))
+  if ((F & kGrad))
     for (int x = threadIdx.x; x < 8 * 256; x += kThreads) hist[x] = 0.f;
   if (warp == kMma) {
     tmem_alloc(&c->tmem_base, kTmemCols);
@@ -702,8 +786,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (n > 0 && ok && wait(&c->mid, 0) && scores(0) && grads(0) && (n == 1 || scores(1))) {
       for (uint32_t t = 0; t < n; ++t) {
-        if (!wait(&c->ds_full, t & 1)) break;
+        if (!wait(&c->dp_free, t & 1)) break;
         if (t + 1 < n && !grads(t + 1)) break;
+        if (!wait(&c->ds_full, t & 1)) break;
         mma_from_tmem(tQ, tmem + (t & 1) * 128, sK(n + t), IDESC_O, t > 0 ? 1u : 0u);
         mma_commit_w(&c->k_empty[(n + t) % RK]);
         if (t + 1 == n) mma_commit_w(&c->o_full);
@@ -718,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mma_commit_w(&c->drain);
     mbar_wait(&c->drain, 0, nullptr, a.spin_ns);
   } else if (warp == kWindow) {
-    if (((F & kBias) && a.table != nullptr)) {
+    if ((F & kBias) && a.table != nullptr) {
       KeyWalk w;
       bool bad = false, ok = true;
       uint32_t t = 0;
@@ -757,10 +842,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x != -INFINITY) nlse = -kLog2e * x;
     }
     uint64_t nlse2 = f2pack(nlse, nlse);
-    const float slope = ((F & kBias) && a.slopes != nullptr) ? a.slopes[h] * kLog2e : 0.f;
-    float far_lo = 0.f, far_hi = 0.f, sum_lo = 0.f, sum_hi = 0.f;
+    const float slope = (F & kBias) && a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
+    float far_lo = 0.f, far_hi = 0.f;
     int n_lo = 0, n_hi = 0;
-    if (((F & kBias) && a.table != nullptr)) {
+    if ((F & kBias) && a.table != nullptr) {
       bool bad = false;
       const __nv_bfloat16* tab = reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
       n_lo = score_bucket(a, -a.R, &bad);
@@ -769,6 +854,64 @@ __global__ void __launch_bounds__(kThreads, 1)
       far_hi = __bfloat162float(tab[n_hi]) * kLog2e;
       if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
     }
+    // What key tile k0 adds to this thread's 64 columns' scores (`near`: window wt & 1).
+    auto bias_of = [&](int k0, bool near, uint32_t wt) {
+      ScoreBias bias = {};
+      if (F & kBias) {
+        bias.wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (wt & 1) * 256 + TILE - 1 - row + half * 64;
+        bias.window = near && c->win_info[wt & 1].cuts > 0;
+        bias.flat = near ? (bias.window ? 0.f : bias.wr[0]) : k0 > p0 ? far_hi : far_lo;
+        bias.side = k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0;
+        bias.slope = slope;
+        bias.off0 = static_cast<float>(k0 + half * 64 - p0 - row);
+      }
+      return bias;
+    };
+    // The table's gradient: 32 columns of dZ, the first at column c0 of the
+    // tile, go to the buckets of their offsets.  While a warp's chunks stay in
+    // one bucket their sums stay in registers; it is added up over the warp
+    // when the bucket changes.  The order is fixed throughout.
+    int cur = 0;
+    float cur_sum = 0.f;
+    auto flush = [&](int next) {
+      if (next != cur) {
+        add_to_bucket(hist + warp * 256 + cur, cur_sum);
+        cur_sum = 0.f;
+        cur = next;
+      }
+    };
+    auto add_buckets = [&](const uint32_t (&g)[32], bool near, int k0, uint32_t wt, int c0) {
+      int bucket = k0 > p0 ? n_hi : n_lo;
+      if (near) {
+        // entries of the window that this warp's 32 rows and 32 columns meet
+        const WindowInfo& info = c->win_info[wt & 1];
+        const int first = TILE - 1 - (w4 * 32 + 31) + c0, last = first + 62;
+        int k = 0, k1 = 0;
+        if (info.cuts <= kMaxCuts) {
+          while (k < info.cuts && info.at[k] <= first) ++k;
+          k1 = k;
+          while (k1 < info.cuts && info.at[k1] <= last) ++k1;
+          bucket = info.bucket[k];
+        }
+        if (info.cuts > kMaxCuts || k != k1) {
+          // (a copy: an array whose address is taken lives in local memory, and
+          // the TMEM load would be stored there before it has arrived)
+          uint32_t copy[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) copy[x] = g[x];
+          if (info.cuts <= kMaxCuts) sum_by_cuts(copy, info, k, k1, TILE - 1 - row + c0, hist + warp * 256);
+          else sum_by_diagonals(copy, smem + L::OFF_BWIN + (wt & 1) * 256 + first, hist + warp * 256);
+          return;
+        }
+      }
+      flush(bucket);
+      uint64_t s = f2pack(0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < 32; x += 2) s = fadd2(s, pair_of(g, x));
+      float lo_, hi_;
+      f2unpack(s, lo_, hi_);
+      cur_sum += lo_ + hi_;
+    };
     bool ok = true;
     uint32_t t = 0, wt = 0;   // wt: windows consumed, over both sweeps
     KeyWalk w;
@@ -780,51 +923,55 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool edge = k0 < tr.z || k0 + TILE > tr.w;
       const bool near = (F & kBias) && is_near(a, k0, p0, p0 + TILE - 1);
       bool got = mbar_wait(&c->a_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
-      if (got && ((F & kBias) && a.table != nullptr)) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && (F & kBias) && a.table != nullptr) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
-      uint32_t r[64], g[64];
-      tmem_ld32(tSh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-      tmem_ld32(tSh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-      tmem_ld32(tSh + 256, *reinterpret_cast<uint32_t(*)[32]>(&g[0]));
-      tmem_ld32(tSh + 288, *reinterpret_cast<uint32_t(*)[32]>(&g[32]));
-      tmem_ld_wait();
-      reg_fence(r);
-      reg_fence(g);
-      tc_fence_before();
-      mbar_arrive(&c->a_free[t & 1]);
       const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;   // columns of the row's interval
-      if (xform) {
-        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (wt & 1) * 256 + TILE - 1 - row + half * 64;
-        const bool window = near && c->win_info[wt & 1].cuts > 0;
-        float none[64];
-        const ScoreBias bias{slope, static_cast<float>(k0 + half * 64 - p0 - row),
-                             k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
-                             near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo};
-        score_columns<F, 1, false, true>(a, terms, r, none, bias, edge ? kExact : kByScore);
-        if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[wt & 1]);
-      }
-      if (edge) {
-#pragma unroll
-        for (int x = 0; x < 64; ++x)
-          if (x < e0 || x >= e1) {
-            r[x] = f2u(-INFINITY);
-            g[x] = 0;
+      const ScoreBias bias = bias_of(k0, near, wt);
+      auto tile = [&](auto cut_c) {
+        constexpr bool CUT = decltype(cut_c)::value != 0;
+        uint64_t s0 = f2pack(0.f, 0.f), s1 = s0;
+#pragma unroll 1
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t r[32], g[32];
+          tmem_ld32(tSh + ch * 32, r);
+          tmem_ld32(tSh + 256 + ch * 32, g);
+          tmem_ld_wait();
+          reg_fence(r);
+          reg_fence(g);
+          if (ch == 1) {
+            tc_fence_before();
+            mbar_arrive(&c->a_free[t & 1]);
           }
-      }
-      uint64_t s0 = f2pack(0.f, 0.f), s1 = s0;
+          const uint32_t bits = CUT ? bits_below(e1 - 32 * ch) & ~bits_below(e0 - 32 * ch) : 0xffffffffu;
+          if (F != 0) {
+            ScoreBias at = bias;
+            at.off0 += static_cast<float>(32 * ch);
+            at.wr += 32 * ch;
+            float none[32];
+            score_columns<F & 3, 1, false, CUT>(a, terms, r, none, at, CUT && ~bits != 0 ? kExact : kByScore);
+          }
+          if (CUT) {
+            keep_bits(r, bits, -INFINITY);
+            keep_bits(g, bits, 0.f);
+          }
 #pragma unroll
-      for (int x = 0; x < 64; x += 2) {
-        float y0, y1;
-        f2unpack(ffma2(f2pack(u2f(r[x]), u2f(r[x + 1])), c2x2, nlse2), y0, y1);
-        const uint64_t pp = f2pack(ex2_approx(y0), ex2_approx(y1)), gg = f2pack(u2f(g[x]), u2f(g[x + 1]));
-        if (x & 2) s1 = ffma2(pp, gg, s1); else s0 = ffma2(pp, gg, s0);
-      }
-      float u0, u1, v0, v1;
-      f2unpack(s0, u0, u1);
-      f2unpack(s1, v0, v1);
-      d_sum += (u0 + u1) + (v0 + v1);
+          for (int x = 0; x < 32; x += 2) {
+            float y0, y1;
+            f2unpack(ffma2(pair_of(r, x), c2x2, nlse2), y0, y1);
+            const uint64_t pp = f2pack(ex2_approx(y0), ex2_approx(y1));
+            if (x & 2) s1 = ffma2(pp, pair_of(g, x), s1); else s0 = ffma2(pp, pair_of(g, x), s0);
+          }
+        }
+        float u0, u1, v0, v1;
+        f2unpack(s0, u0, u1);
+        f2unpack(s1, v0, v1);
+        d_sum += (u0 + u1) + (v0 + v1);
+      };
+      if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) tile(IntC<1>{});
+      else tile(IntC<0>{});
+      if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[wt & 1]);
       more = w.next >= 0;
       if (more) key_next(a, h, qb, w);
     }
@@ -855,145 +1002,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool near = (F & kBias) && is_near(a, k0, p0, p0 + TILE - 1);
       const uint32_t u = wt;   // position in the K ring
       bool got = mbar_wait(&c->s_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
-      if (got && ((F & kBias) && a.table != nullptr)) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && (F & kBias) && a.table != nullptr) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
       if (got && edge) got = mbar_wait(&c->k_full[u % RK], (u / RK) & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
-      uint32_t r[64];
-      tmem_ld32(tSh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-      tmem_ld32(tSh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-      tmem_ld_wait();
-      reg_fence(r);
-      float f[64];
       const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;   // columns of the row's interval
-      if (xform) {
-        const float* wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (wt & 1) * 256 + TILE - 1 - row + half * 64;
-        const bool window = near && c->win_info[wt & 1].cuts > 0;
-        const ScoreBias bias{slope, static_cast<float>(k0 + half * 64 - p0 - row),
-                             k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0, window, wr,
-                             near ? (window ? 0.f : wr[0]) : k0 > p0 ? far_hi : far_lo};
-        score_columns<F, 1, true, true>(a, terms, r, f, bias, edge ? kExact : kByScore);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 64; ++x) f[x] = 1.f;
-      }
-      if (edge && half < D / 64) {
+      const ScoreBias bias = bias_of(k0, near, wt);
+      auto tile = [&](auto cut_c) {
+        constexpr bool CUT = decltype(cut_c)::value != 0;
         // Keys with a NaN or an infinity: zeroed before dQ reads them (S, which
         // is complete, has made a visible one's dS NaN).
-        clean_box_row(smem + L::OFF_K + (u % RK) * L::TB + half * L::BOX + row * 128, row);
-        fence_proxy_async_smem();
-      }
-      float p[64];
-#pragma unroll
-      for (int x = 0; x < 64; x += 2) {
-        float y0, y1;
-        f2unpack(ffma2(f2pack(u2f(r[x]), u2f(r[x + 1])), c2x2, nlse2), y0, y1);
-        p[x] = ex2_approx(y0);
-        p[x + 1] = ex2_approx(y1);
-      }
-      ok = __all_sync(0xffffffffu, mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns));
-      if (!ok) break;
-      tc_fence_after();
-      tmem_ld32(tPh, *reinterpret_cast<uint32_t(*)[32]>(&r[0]));
-      tmem_ld32(tPh + 32, *reinterpret_cast<uint32_t(*)[32]>(&r[32]));
-      tmem_ld_wait();
-      reg_fence(r);
-#pragma unroll
-      for (int x = 0; x < 64; x += 2)
-        f2unpack(fmul2(fadd2(f2pack(u2f(r[x]), u2f(r[x + 1])), nd2), f2pack(p[x], p[x + 1])), p[x], p[x + 1]);
-      if (edge) {
-#pragma unroll
-        for (int x = 0; x < 64; ++x)
-          if (x < e0 || x >= e1) p[x] = f[x] = 0.f;   // the factor of a masked score may be NaN
-      }
-      if (((F & kBias) && a.dtable != nullptr)) {   // p is dZ
-        const WindowInfo& info = c->win_info[wt & 1];
-        if (near && info.cuts <= kMaxCuts) {
-          // Few buckets in the tile pair's offsets: the row's sums up to each
-          // boundary (column x is entry 127 - row + 64 half + x), their
-          // differences added up over the warp in a fixed order.
-          float below[kMaxCuts + 1];
-#pragma unroll
-          for (int k = 0; k < kMaxCuts; ++k) {
-            if (k >= info.cuts) { below[k] = 0.f; continue; }
-            const int cut = info.at[k] - (TILE - 1 - row + half * 64);
-            float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-            for (int x = 0; x < 64; x += 2) {
-              if (x < cut) s0 += p[x];
-              if (x + 1 < cut) s1 += p[x + 1];
-            }
-            below[k] = s0 + s1;
-          }
-          float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-          for (int x = 0; x < 64; x += 2) {
-            s0 += p[x];
-            s1 += p[x + 1];
-          }
-          below[kMaxCuts] = s0 + s1;
-          float before = 0.f;
-#pragma unroll
-          for (int k = 0; k <= kMaxCuts; ++k) {
-            if (k > info.cuts) break;
-            const float upto = k == info.cuts ? below[kMaxCuts] : below[k < kMaxCuts ? k : 0];
-            float v = upto - before;
-            before = upto;
-#pragma unroll
-            for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
-            if (lane == 31) hist[warp * 256 + info.bucket[k]] += v;
-          }
-        } else if (near) {
-          // Sums along the diagonals (one offset each) by passing a running
-          // sum from row to row: after column x lane 31 holds the sum of the
-          // diagonal that ends in it; 31 more steps drain the others.  Runs of
-          // offsets of one bucket are added up before the warp's own
-          // accumulators are touched, so the order is fixed.
-          const uint8_t* bw = smem + L::OFF_BWIN + (wt & 1) * 256 + half * 64 + 96 - w4 * 32;
-          float* acc = hist + warp * 256;
-          float diag = 0.f, run = 0.f;
-          int cur = bw[0];
-          auto add = [&](int x) {
-            const int n = bw[x];
-            if (n != cur) {
-              if (lane == 31) acc[cur] += run;
-              run = 0.f;
-              cur = n;
-            }
-            run += diag;
-          };
-#pragma unroll
-          for (int x = 0; x < 64; ++x) {
-            const float up = __shfl_up_sync(0xffffffffu, diag, 1);
-            diag = p[x] + (lane == 0 ? 0.f : up);
-            add(x);
-          }
+        if (CUT && edge && half < D / 64) clean_row<1>(smem + L::OFF_K + (u % RK) * L::TB + half * L::BOX, row);
+        ok = __all_sync(0xffffffffu, mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns));
+        if (!ok) return;
+        tc_fence_after();
 #pragma unroll 1
-          for (int x = 64; x < 95; ++x) {
-            const float up = __shfl_up_sync(0xffffffffu, diag, 1);
-            diag = lane == 0 ? 0.f : up;
-            add(x);
+        for (int ch = 0; ch < 2; ++ch) {
+          uint32_t r[32], g[32];
+          tmem_ld32(tSh + ch * 32, r);
+          tmem_ld32(tPh + ch * 32, g);
+          tmem_ld_wait();
+          reg_fence(r);
+          reg_fence(g);
+          if (ch == 1) {
+            tc_fence_before();
+            mbar_arrive(&c->dp_free);
           }
-          if (lane == 31) acc[cur] += run;
-          __syncwarp();
-        } else {
-          float s0 = 0.f, s1 = 0.f;
+          const uint32_t bits = CUT ? bits_below(e1 - 32 * ch) & ~bits_below(e0 - 32 * ch) : 0xffffffffu;
+          float f[32];
+          if (F != 0) {
+            ScoreBias at = bias;
+            at.off0 += static_cast<float>(32 * ch);
+            at.wr += 32 * ch;
+            score_columns<F & 3, 1, (F & kCap) != 0, CUT>(a, terms, r, f, at, CUT && ~bits != 0 ? kExact : kByScore);
+          }
+          // dZ = P (dP - D) in place of dP
 #pragma unroll
-          for (int x = 0; x < 64; x += 2) {
-            s0 += p[x];
-            s1 += p[x + 1];
+          for (int x = 0; x < 32; x += 2) {
+            float y0, y1;
+            f2unpack(ffma2(pair_of(r, x), c2x2, nlse2), y0, y1);
+            set_pair(g, x, fmul2(fadd2(pair_of(g, x), nd2), f2pack(ex2_approx(y0), ex2_approx(y1))));
           }
-          if (k0 > p0) sum_hi += s0 + s1; else sum_lo += s0 + s1;
+          if (CUT) {
+            keep_bits(g, bits, 0.f);
+            if (F & kCap) {   // the factor of a masked score may be NaN
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (!(bits & (1u << x))) f[x] = 0.f;
+            }
+          }
+          if (F & kGrad) add_buckets(g, near, k0, wt, half * 64 + ch * 32);
+          uint32_t pk[16];
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            float y0, y1;
+            uint64_t v = pair_of(g, x);
+            if (F & kCap) v = fmul2(v, f2pack(f[x], f[x + 1]));
+            f2unpack(v, y0, y1);
+            pk[x / 2] = pack_bf16x2(y0, y1);
+          }
+          tmem_st16(tSh + ch * 16, pk);
         }
-      }
-      if (((F & kBias) && a.table != nullptr)) mbar_arrive(&c->win_empty[wt & 1]);
-#pragma unroll
-      for (int x = 0; x < 64; ++x) p[x] *= f[x];
-      store_half(tSh, p);
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&c->ds_full);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&c->ds_full);
+      };
+      if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) tile(IntC<1>{});
+      else tile(IntC<0>{});
+      if (!ok) break;
+      if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[wt & 1]);
       more = w.next >= 0;
       if (more) key_next(a, h, qb, w);
     }
@@ -1012,23 +1090,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       c->abort = 1;
       report_status(a.status, CALIBATT_E_TIMEOUT);
     }
-    if (((F & kBias) && a.dtable != nullptr)) {
-#pragma unroll
-      for (int m = 16; m > 0; m >>= 1) {
-        sum_lo += __shfl_xor_sync(0xffffffffu, sum_lo, m);
-        sum_hi += __shfl_xor_sync(0xffffffffu, sum_hi, m);
-      }
-      if (lane == 31) {
-        hist[warp * 256 + n_lo] += sum_lo;
-        hist[warp * 256 + n_hi] += sum_hi;
-      }
+    if ((F & kGrad)) {
+      flush(-1);
     }
   }
 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (((F & kBias) && a.dtable != nullptr)) {
+  if ((F & kGrad)) {
     float* dst = a.part_table + ((static_cast<size_t>(b) * a.H + h) * a.table_tiles + qb) * a.n_buckets;
     for (int n = threadIdx.x; n < a.n_buckets; n += kThreads) {
       float s = 0.f;
@@ -1050,12 +1120,13 @@ int launch(const ScoreArgs& a, cudaStream_t s) {
   if ((rc = make_tmap4_bf16(&to, a.dout, a.B, a.H, a.Nq, D, TILE, 1))) return rc;
   const long long nk = static_cast<long long>(a.B) * a.Hkv * a.nkb, nq = static_cast<long long>(a.B) * a.H * a.nqb;
   if (nk >= (1ll << 31) || nq >= (1ll << 31)) return set_error(CALIBATT_E_UNSUPPORTED, "too many tiles");
-  static std::atomic<bool> done_kv[kMaxDevices], done_q[kMaxDevices];
+  static std::atomic<bool> done_kv[kMaxDevices], done_q[2][kMaxDevices];
   auto dkv = k_score_dkv<D, F>;
   auto dq = k_score_dq<D, F>;
+  if ((F & kBias) && a.dtable != nullptr) dq = k_score_dq<D, F & kBias ? F | kGrad : F>;
   if ((rc = configure_kernel(reinterpret_cast<const void*>(dkv), done_kv, DkvLayout<D>::SMEM, kLaunchRegs, "k_score_dkv")))
     return rc;
-  if ((rc = configure_kernel(reinterpret_cast<const void*>(dq), done_q, DqLayout<D>::SMEM, kLaunchRegs, "k_score_dq")))
+  if ((rc = configure_kernel(reinterpret_cast<const void*>(dq), done_q[a.dtable != nullptr], DqLayout<D>::SMEM, kLaunchRegs, "k_score_dq")))
     return rc;
   dq<<<static_cast<unsigned>(nq), kThreads, DqLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
   dkv<<<static_cast<unsigned>(nk), kThreads, DkvLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);

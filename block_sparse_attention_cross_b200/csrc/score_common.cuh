@@ -159,6 +159,30 @@ __device__ __forceinline__ bool key_start(const ScoreArgs& a, int h, int qb, int
   return true;
 }
 
+// Columns below n of a chunk of 32, as bits.
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+
+// Columns whose bit is 0 become `value`.
+__device__ __forceinline__ void keep_bits(uint32_t (&r)[32], uint32_t bits, float value) {
+#pragma unroll
+  for (int x = 0; x < 32; ++x)
+    if (!(bits & (1u << x))) r[x] = f2u(value);
+}
+
+// The boxes of row `row` of a tile of 128 rows: each zeroed where it holds a
+// NaN or an infinity; whether one did.  Out of line: only tiles that the mask
+// cuts need it.
+template <int BOXES>
+__device__ __noinline__ bool clean_row(uint8_t* tile, int row) {
+  bool bad = false;
+#pragma unroll 1
+  for (int x = 0; x < BOXES; ++x) bad |= clean_box_row(tile + x * 128 * 128 + row * 128, row);
+  fence_proxy_async_smem();
+  return bad;
+}
+
 // ---- the table's values along the offsets of a tile pair ---------------------
 // A tile pair meets 255 offsets; entry x of a window is offset o0 + x.  Far
 // from zero a logarithmic bucket spans many offsets, so a window often holds
@@ -285,19 +309,21 @@ __device__ __forceinline__ float score_extent(const uint32_t (&r)[N]) {
 }
 
 // The capped score by the polynomial, plus `shift`; f: the cap's derivative.
-template <bool FACTOR, int N>
+template <bool FACTOR, bool BIAS, int N>
 __device__ __forceinline__ void cap_polynomial(const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N], float shift) {
   const uint64_t c0 = f2pack(t.c[0], t.c[0]), c1 = f2pack(t.c[1], t.c[1]), c2 = f2pack(t.c[2], t.c[2]),
                  c3 = f2pack(t.c[3], t.c[3]), c4 = f2pack(t.c[4], t.c[4]), shift2 = f2pack(shift, shift);
-  const uint64_t iv = f2pack(t.inv, t.inv), one = f2pack(1.f, 1.f), neg = f2pack(-1.f, -1.f);
+  const uint64_t ninv2 = f2pack(-t.inv * t.inv, -t.inv * t.inv), one = f2pack(1.f, 1.f);
 #pragma unroll
   for (int x = 0; x < N; x += 2) {
     const uint64_t s = pair_of(r, x), v = fmul2(s, s);
     const uint64_t q = ffma2(ffma2(ffma2(ffma2(c4, v, c3), v, c2), v, c1), v, c0);
-    set_pair(r, x, ffma2(s, q, shift2));
     if (FACTOR) {
-      const uint64_t th = fmul2(fmul2(s, q), iv);
-      f2unpack(ffma2(fmul2(th, neg), th, one), f[x], f[x + 1]);
+      const uint64_t y = fmul2(s, q);
+      f2unpack(ffma2(fmul2(y, y), ninv2, one), f[x], f[x + 1]);
+      set_pair(r, x, BIAS ? fadd2(y, shift2) : y);
+    } else {
+      set_pair(r, x, ffma2(s, q, shift2));
     }
   }
 }
@@ -325,7 +351,7 @@ __device__ __forceinline__ void score_columns(const ScoreArgs& a, const ScoreTer
   const float sl = b.side > 0 ? -b.slope : b.slope;   // -slope |off0 + DIR x| = sl (off0 + DIR x)
   const float shift = F & kBias ? (b.window ? 0.f : b.flat) + (linear ? sl * b.off0 : 0.f) : 0.f;
   if (F & kCap) {
-    if (form == kAny || (form == kByScore && score_extent(r) <= t.small)) cap_polynomial<FACTOR>(t, r, f, shift);
+    if (form == kAny || (form == kByScore && score_extent(r) <= t.small)) cap_polynomial<FACTOR, (F & kBias) != 0>(t, r, f, shift);
     else cap_mufu<FACTOR>(t, r, f, shift);
   } else {
     const uint64_t sc = f2pack(t.sc, t.sc), shift2 = f2pack(shift, shift);

@@ -175,28 +175,6 @@ constexpr int kFew = 8;
 // (|v| < 2^20) inside fp32, and bf16 has fp32's exponents.
 constexpr float kBoundedCap = 80.f;
 
-// Columns below n of a chunk of 32, as bits.
-__device__ __forceinline__ uint32_t bits_below(int n) {
-  return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
-}
-
-// Columns whose bit is 0 become `value`.
-__device__ __forceinline__ void keep_bits(uint32_t (&r)[32], uint32_t bits, float value) {
-#pragma unroll
-  for (int x = 0; x < 32; ++x)
-    if (!(bits & (1u << x))) r[x] = f2u(value);
-}
-
-// Row `row` of a V tile: zeroed where a 64-column box of it holds a NaN or an infinity; whether one did.
-template <int D>
-__device__ __noinline__ bool clean_row(uint8_t* tile, int row) {
-  bool bad = false;
-#pragma unroll 1
-  for (int x = 0; x < D / 64; ++x) bad |= clean_box_row(tile + x * TILE * 128 + row * 128, row);
-  fence_proxy_async_smem();
-  return bad;
-}
-
 template <int D, int F>
 __global__ void __launch_bounds__(kThreads, 1)
     k_score_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -518,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu,
                           mbar_wait(&c->ring_full[slot][ge % R], (ge / R) & 1, &c->abort, a.spin_ns));
           if (!ok) break;
-          const bool bad = clean_row<D>(smem + L::OFF_RING + (slot * R + ge % R) * L::TBYTES, row);
+          const bool bad = clean_row<D / 64>(smem + L::OFF_RING + (slot * R + ge % R) * L::TBYTES, row);
           const uint32_t bw = __ballot_sync(0xffffffffu, bad);
           if (lane == 0) c->bad[slot][gb & 1][w4] = bw;
           scanned = true;
