@@ -372,8 +372,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         far = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n]) * kLog2e;
         if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
       }
-      bool got = mbar_wait(&c->s_full, t & 1, &c->abort, a.spin_ns) &&
-                 mbar_wait(&c->ring_full[e], (t / R) & 1, &c->abort, a.spin_ns);
+      // The row terms of the first 32 queries are read before the wait for the
+      // scores, those of the next 32 a chunk ahead: the tensor core's operand
+      // reads keep shared memory busy, and a read between two exponentials
+      // stalls them (1950 against 1400 cycles a tile pair).
+      bool got = mbar_wait(&c->ring_full[e], (t / R) & 1, &c->abort, a.spin_ns);
+      float4 nl[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) nl[x] = nlse[x];
+      got = got && mbar_wait(&c->s_full, t & 1, &c->abort, a.spin_ns);
       if (got && (F & kBias) && a.table != nullptr) got = mbar_wait(&c->win_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
       if (got && edge) got = mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
@@ -426,12 +433,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c32 = 0; c32 < 2; ++c32) {
           const uint32_t seen = c32 ? seen1 : seen0;
           float pv[32];
+          float4 ahead[8];
+          if (c32 == 0) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) ahead[x] = nlse[8 + x];
+          }
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
-            const float4 nl = nlse[c32 * 8 + x / 4];
+            const float4 n4 = nl[x / 4];
             const int o = c32 * 32 + x;
-            f2unpack(ffma2(pair_of(r, o), c2x2, f2pack(nl.x, nl.y)), pv[x], pv[x + 1]);
-            f2unpack(ffma2(pair_of(r, o + 2), c2x2, f2pack(nl.z, nl.w)), pv[x + 2], pv[x + 3]);
+            f2unpack(ffma2(pair_of(r, o), c2x2, f2pack(n4.x, n4.y)), pv[x], pv[x + 1]);
+            f2unpack(ffma2(pair_of(r, o + 2), c2x2, f2pack(n4.z, n4.w)), pv[x + 2], pv[x + 3]);
+          }
+          if (c32 == 0) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) nl[x] = ahead[x];
           }
           uint32_t pk[16];
 #pragma unroll
@@ -456,6 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&c->p_full);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) nl[x] = nd[x];
         ok = __all_sync(0xffffffffu, mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns));
         if (!ok) return;
         tc_fence_after();
@@ -467,9 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c32 = 0; c32 < 2; ++c32) {
           const uint32_t seen = c32 ? seen1 : seen0;
           uint32_t pk[16];
+          float4 ahead[8];
+          if (c32 == 0) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) ahead[x] = nd[8 + x];
+          }
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
-            const float4 d4 = nd[c32 * 8 + x / 4];
+            const float4 d4 = nl[x / 4];
             const int o = c32 * 32 + x;
             float y0, y1, y2, y3;
             f2unpack(fmul2(fadd2(pair_of(r, o), f2pack(d4.x, d4.y)), f2pack(pf[o], pf[o + 1])), y0, y1);
@@ -484,6 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[x / 2 + 1] = pack_bf16x2(y2, y3);
           }
           tmem_st16(tPh + c32 * 16, pk);
+          if (c32 == 0) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) nl[x] = ahead[x];
+          }
         }
         tmem_st_wait();
         tc_fence_before();
