@@ -170,6 +170,9 @@ constexpr int kBounded = 4;
 // At most 32 rows, repeated in the four lane quarters (a kernel of its own, so
 // that neither form carries the other's code).
 constexpr int kFew = 8;
+// Key tiles whose scores the mask leaves whole; that it cuts (or where the
+// distance passes 0); and whole ones with one table value and no other term.
+enum TileKind { kFullTile, kCutTile, kFlatTile };
 // Largest cap in log2 units that goes without a maximum: probabilities
 // 2^score lie in 2^+-80, their sums over 2^24 keys and their products with V
 // (|v| < 2^20) inside fp32, and bf16 has fp32's exponents.
@@ -410,8 +413,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = t_s + 128;
     // Scores are in log2 units.
     const ScoreTerms terms = score_terms(a);
-    const float c2 = (F & 3) == 0 ? terms.sc : 1.f;   // plain scores: the scale is folded into the exponent
-    const uint64_t c2x2 = f2pack(c2, c2);
     uint32_t gb = 0;
     int tiles = 0;
     bool ok = true, corrupt = false;
@@ -525,13 +526,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         float alpha = 1.f;
         bool rescale = false;
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
-        const int ch0 = FEW ? w4 : 0, ch1 = FEW ? w4 + 1 : 4;   // this warp's chunks
         auto softmax = [&](auto cut_c) {
-          constexpr bool CUT = decltype(cut_c)::value != 0;
-          uint32_t r[32];
+          constexpr bool CUT = decltype(cut_c)::value == kCutTile;
+          // raw scores in both passes: no terms, or one table value for the whole tile
+          constexpr bool RAW = (F & 3) == 0 || decltype(cut_c)::value == kFlatTile;
+          // columns of a chunk: 64 where the code is short (plain 904 against 925
+          // us), else 32 (capped 1137 against 1207 us, a table 1199 against 1342)
+          constexpr int W = RAW && !CUT && !FEW ? 64 : 32;
+          const float scale = RAW ? terms.sc : 1.f, offset = RAW && (F & 3) ? bias.flat : 0.f;
+          uint32_t r[W];
           uint32_t dead = 0;   // chunks that no row of the warp sees
           auto load = [&](int ch) {
-            tmem_ld32(t_s + ch * 32, r);
+#pragma unroll
+            for (int x = 0; x < W; x += 32) tmem_ld32(t_s + ch * W + x, *reinterpret_cast<uint32_t(*)[32]>(&r[x]));
             tmem_ld_wait();
             reg_fence(r);
           };
@@ -539,40 +546,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto transform = [&](int ch) {
             const uint32_t bits = CUT ? bits_below(e1 - 32 * ch) & ~bits_below(e0 - 32 * ch) : 0xffffffffu;
             if (CUT && !__any_sync(0xffffffffu, bits != 0)) return false;
-            if ((F & 3) != 0) {
+            if (!RAW) {
               ScoreBias at = bias;
-              at.off0 += static_cast<float>(32 * ch);
-              at.wr += 32 * ch;
-              float none[32];
+              at.off0 += static_cast<float>(W * ch);
+              at.wr += W * ch;
+              float none[W];
               score_columns<F & 3, 1, false, CUT>(a, terms, r, none, at,
                                                  !live ? kAny : CUT && ~bits != 0 ? kExact : kByScore);
             }
-            if (CUT) keep_bits(r, bits, -INFINITY);
+            if constexpr (CUT) keep_bits(r, bits, -INFINITY);
             return true;
           };
           if (!(F & kBounded)) {
             // First pass: (transformed) scores and the tile's maximum.
             float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll 1
-            for (int ch = ch0; ch < ch1; ++ch) {
+            for (int ch = FEW ? w4 : 0; ch < (FEW ? w4 + 1 : TILE / W); ++ch) {
               load(ch);
               if (!transform(ch)) {
                 dead |= 1u << ch;
                 continue;
               }
 #pragma unroll
-              for (int x = 0; x < 32; x += 4) {
+              for (int x = 0; x < W; x += 4) {
                 mx0 = fmax3(mx0, u2f(r[x]), u2f(r[x + 1]));
                 mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
               }
-              if (((F & 3) != 0 || CUT) && !FEW) tmem_st32(t_s + ch * 32, r);   // one chunk stays in registers
+              if ((!RAW || CUT) && !FEW) {   // one chunk stays in registers
+#pragma unroll
+                for (int x = 0; x < W; x += 32) tmem_st32(t_s + ch * W + x, *reinterpret_cast<uint32_t(*)[32]>(&r[x]));
+              }
             }
-            const float bmax = fmaxf(mx0, mx1);
-            best = fmaxf(best, bmax);
+            const float m_cand = fmaf(fmaxf(mx0, mx1), scale, offset);
+            best = fmaxf(best, m_cand);
             // The reference: the first tile's maximum, raised (and O and l
             // rescaled) only by more than the threshold.  While a row has seen
             // nothing it is -inf and the exponent's shift 0.
-            const float m_cand = bmax * c2;
             if (first) {
               m = m_cand;
             } else {
@@ -583,16 +592,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 m = m_cand;
               }
             }
-            if (((F & 3) != 0 || CUT) && !FEW) tmem_st_wait();
+            if ((!RAW || CUT) && !FEW) tmem_st_wait();
           }
           // Second pass: probabilities, stored as bf16 pairs over the scores
           // already read, and their fp32 sum.
-          const float neg = m == -INFINITY ? 0.f : -m;
-          const uint64_t negm = f2pack(neg, neg);
+          const float neg = (m == -INFINITY ? 0.f : -m) + offset;
+          const uint64_t negm = f2pack(neg, neg), scale2 = f2pack(scale, scale);
           float pm0 = 0.f, pm1 = 0.f;
 #pragma unroll 1
-          for (int ch = ch0; ch < ch1; ++ch) {
-            uint32_t pk[16];
+          for (int ch = FEW ? w4 : 0; ch < (FEW ? w4 + 1 : TILE / W); ++ch) {
+            uint32_t pk[W / 2];
             bool some = true;
             if (!CUT || !((dead >> ch) & 1u)) {
               if ((F & kBounded) || !FEW) load(ch);
@@ -600,16 +609,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
               some = false;
             }
-            if (CUT && !some) {
+            if constexpr (CUT) {
+              if (!some) {
 #pragma unroll
-              for (int x = 0; x < 16; ++x) pk[x] = 0;
-              tmem_st16(t_s + ch * 16, pk);
-              continue;
+                for (int x = 0; x < 16; ++x) pk[x] = 0;
+                tmem_st16(t_s + ch * 16, pk);
+                continue;
+              }
             }
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
+            for (int x = 0; x < W / 2; ++x) {
               uint64_t y = pair_of(r, 2 * x);
-              if (!(F & kBounded)) y = ffma2(y, c2x2, negm);
+              if (!(F & kBounded)) y = ffma2(y, scale2, negm);
               float xl, xh;
               f2unpack(y, xl, xh);
               xl = ex2_approx(xl);
@@ -621,12 +632,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               pk[x] = pack_bf16x2(xl, xh);
             }
-            tmem_st16(t_s + ch * 16, pk);
+#pragma unroll
+            for (int x = 0; x < W / 2; x += 16)
+              tmem_st16(t_s + ch * (W / 2) + x, *reinterpret_cast<uint32_t(*)[16]>(&pk[x]));
           }
           if (F & kBounded) best = fmaxf(best, fmaxf(pm0, pm1));
         };
-        if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) softmax(IntC<1>{});
-        else softmax(IntC<0>{});
+        if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) softmax(IntC<kCutTile>{});
+        else if ((F & 3) == kBias && a.slopes == nullptr && !bias.window) softmax(IntC<kFlatTile>{});
+        else softmax(IntC<kFullTile>{});
         if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[slot][gb & 1]);
         if (FEW) {   // the other warps' columns are 0 in these lanes
           uint32_t pk[16];
@@ -665,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---- epilogue: O / l, LSE.  As in the block-sparse forward, the
       // rounding error of the row's largest probability moves into the
       // normaliser, so that a row with one dominant key returns its value.
-      const float p_best = F & kBounded ? best : ex2_approx(fmaf(best, c2, -m));
+      const float p_best = F & kBounded ? best : ex2_approx(best - m);
       const float corr = __uint_as_float(pack_bf16x2(p_best, 0.f) << 16) - p_best;
       ok = __all_sync(0xffffffffu, mbar_wait(&c->o_full[slot], tiles & 1, &c->abort, a.spin_ns));
       if (!ok) break;
