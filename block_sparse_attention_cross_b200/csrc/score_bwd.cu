@@ -327,13 +327,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       QueryWalk w;
       bool bad = false, ok = true;
       uint32_t t = 0;
-      for (bool more = query_start(a, b, hk, kb, w); more; more = query_next(a, b, hk, kb, w), ++t) {
-        const int e = t & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&c->win_empty[e], ((t >> 1) & 1) ^ 1, &c->abort, a.spin_ns));
-        if (!ok) break;
+      for (bool more = query_start(a, b, hk, kb, w); more; more = query_next(a, b, hk, kb, w)) {
         const int p0 = a.q_start[b] + w.qb * TILE;
-        if (is_near(a, k0, p0, p0 + TILE - 1))
-          fill_window(a, hk * a.G + w.g, 1, k0 - p0 - (TILE - 1), reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256, nullptr,
+        if (!is_near(a, k0, p0, p0 + TILE - 1)) continue;
+        const int e = t & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&c->win_empty[e], ((t >> 1) & 1) ^ 1, &c->abort,
+                                                  kWindowPatience * a.spin_ns));
+        if (!ok) break;
+        ++t;
+        fill_window(a, hk * a.G + w.g, 1, k0 - p0 - (TILE - 1), reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256, nullptr,
                       &c->win_info[e], &bad);
         mbar_arrive(&c->win_full[e]);
       }
@@ -353,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c2x2 = f2pack(xform ? 1.f : terms.sc, xform ? 1.f : terms.sc);
     const int j = k0 + row;
     bool ok = true;
-    uint32_t t = 0;
+    uint32_t t = 0, nw = 0;   // pairs and windows consumed
     QueryWalk w;
     for (bool more = query_start(a, b, hk, kb, w); more; more = query_next(a, b, hk, kb, w), ++t) {
       const int e = t % R, h = hk * a.G + w.g;
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int x = 0; x < 8; ++x) nl[x] = nlse[x];
       got = got && mbar_wait(&c->s_full, t & 1, &c->abort, a.spin_ns);
-      if (got && (F & kBias) && a.table != nullptr) got = mbar_wait(&c->win_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && near) got = mbar_wait(&c->win_full[nw & 1], (nw >> 1) & 1, &c->abort, a.spin_ns);
       if (got && edge) got = mbar_wait(&c->dp_full, t & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
@@ -389,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // column x: query 64 half + x, offset j - p falls with x
       ScoreBias bias = {};
       if (F & kBias) {
-        bias.wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (t & 1) * 256 + row + TILE - 1 - half * 64;
-        bias.window = near && c->win_info[t & 1].cuts > 0;
+        bias.wr = reinterpret_cast<const float*>(smem + L::OFF_WIN) + (nw & 1) * 256 + row + TILE - 1 - half * 64;
+        bias.window = near && c->win_info[nw & 1].cuts > 0;
         bias.flat = near ? (bias.window ? 0.f : bias.wr[0]) : far;
         bias.side = k0 >= p0 + TILE - 1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0;
         bias.slope = slope;
@@ -426,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float pf[64];   // first the cap's factor, then P times it
         if (F != 0) {
           score_columns<F, -1, true, CUT>(a, terms, r, pf, bias, CUT && edge ? kExact : kByScore);
-          if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[t & 1]);
+          if (near) mbar_arrive(&c->win_empty[nw & 1]);
         }
         // P, rounded to bf16 for dV, and P times the cap's factor kept for dS
 #pragma unroll
@@ -519,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) pair(IntC<1>{});
       else pair(IntC<0>{});
       if (!ok) break;
+      if (near) ++nw;
     }
     // ---- epilogue: warpgroup 0 writes dV, warpgroup 1 dK ---------------------
     const bool live = j < a.Nk;
@@ -835,14 +838,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool bad = false, ok = true;
       uint32_t t = 0;
       int sweep = 0;
-      for (bool more = key_start(a, h, qb, lo, hi, w); more; ++t) {
-        const int e = t & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&c->win_empty[e], ((t >> 1) & 1) ^ 1, &c->abort, a.spin_ns));
-        if (!ok) break;
-        if (is_near(a, w.kb * TILE, p0, p0 + TILE - 1))
+      for (bool more = key_start(a, h, qb, lo, hi, w); more;) {
+        if (is_near(a, w.kb * TILE, p0, p0 + TILE - 1)) {
+          const int e = t & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&c->win_empty[e], ((t >> 1) & 1) ^ 1, &c->abort,
+                                                  kWindowPatience * a.spin_ns));
+          if (!ok) break;
           fill_window(a, h, 1, w.kb * TILE - p0 - (TILE - 1), reinterpret_cast<float*>(smem + L::OFF_WIN) + e * 256,
                       smem + L::OFF_BWIN + e * 256, &c->win_info[e], &bad);
-        mbar_arrive(&c->win_full[e]);
+          mbar_arrive(&c->win_full[e]);
+          ++t;
+        }
         if (w.next >= 0) key_next(a, h, qb, w);
         else more = sweep++ == 0 && key_start(a, h, qb, lo, hi, w);
       }
@@ -881,7 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       far_hi = __bfloat162float(tab[n_hi]) * kLog2e;
       if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
     }
-    // What key tile k0 adds to this thread's 64 columns' scores (`near`: window wt & 1).
+    // What key tile k0 adds to this thread's 64 columns' scores (`near`: from window wt & 1).
     auto bias_of = [&](int k0, bool near, uint32_t wt) {
       ScoreBias bias = {};
       if (F & kBias) {
@@ -940,7 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       cur_sum += lo_ + hi_;
     };
     bool ok = true;
-    uint32_t t = 0, wt = 0;   // wt: windows consumed, over both sweeps
+    uint32_t t = 0, wt = 0, nw = 0;   // wt, nw: tiles and windows consumed, over both sweeps
     KeyWalk w;
     // ---- first sweep: D = sum over the visible keys of P dP ------------------
     float d_sum = 0.f;
@@ -950,12 +956,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool edge = k0 < tr.z || k0 + TILE > tr.w;
       const bool near = (F & kBias) && is_near(a, k0, p0, p0 + TILE - 1);
       bool got = mbar_wait(&c->a_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
-      if (got && (F & kBias) && a.table != nullptr) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && near) got = mbar_wait(&c->win_full[nw & 1], (nw >> 1) & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
       const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;   // columns of the row's interval
-      const ScoreBias bias = bias_of(k0, near, wt);
+      const ScoreBias bias = bias_of(k0, near, nw);
       auto tile = [&](auto cut_c) {
         constexpr bool CUT = decltype(cut_c)::value != 0;
         uint64_t s0 = f2pack(0.f, 0.f), s1 = s0;
@@ -998,7 +1004,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) tile(IntC<1>{});
       else tile(IntC<0>{});
-      if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[wt & 1]);
+      if (near) {
+        mbar_arrive(&c->win_empty[nw & 1]);
+        ++nw;
+      }
       more = w.next >= 0;
       if (more) key_next(a, h, qb, w);
     }
@@ -1029,13 +1038,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool near = (F & kBias) && is_near(a, k0, p0, p0 + TILE - 1);
       const uint32_t u = wt;   // position in the K ring
       bool got = mbar_wait(&c->s_full[t & 1], (t >> 1) & 1, &c->abort, a.spin_ns);
-      if (got && (F & kBias) && a.table != nullptr) got = mbar_wait(&c->win_full[wt & 1], (wt >> 1) & 1, &c->abort, a.spin_ns);
+      if (got && near) got = mbar_wait(&c->win_full[nw & 1], (nw >> 1) & 1, &c->abort, a.spin_ns);
       if (got && edge) got = mbar_wait(&c->k_full[u % RK], (u / RK) & 1, &c->abort, a.spin_ns);
       ok = __all_sync(0xffffffffu, got);
       if (!ok) break;
       tc_fence_after();
       const int e0 = vis.x - k0 - half * 64, e1 = vis.y - k0 - half * 64;   // columns of the row's interval
-      const ScoreBias bias = bias_of(k0, near, wt);
+      const ScoreBias bias = bias_of(k0, near, nw);
       auto tile = [&](auto cut_c) {
         constexpr bool CUT = decltype(cut_c)::value != 0;
         // Keys with a NaN or an infinity: zeroed before dQ reads them (S, which
@@ -1079,7 +1088,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!(bits & (1u << x))) f[x] = 0.f;
             }
           }
-          if (F & kGrad) add_buckets(g, near, k0, wt, half * 64 + ch * 32);
+          if (F & kGrad) add_buckets(g, near, k0, nw, half * 64 + ch * 32);
           uint32_t pk[16];
 #pragma unroll
           for (int x = 0; x < 32; x += 2) {
@@ -1098,7 +1107,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) tile(IntC<1>{});
       else tile(IntC<0>{});
       if (!ok) break;
-      if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[wt & 1]);
+      if (near) {
+        mbar_arrive(&c->win_empty[nw & 1]);
+        ++nw;
+      }
       more = w.next >= 0;
       if (more) key_next(a, h, qb, w);
     }

@@ -196,6 +196,10 @@ struct WindowInfo {
   int pad[2];
 };
 
+// The warp that fills the windows runs up to two windows ahead, and a walk may
+// hold many tiles that need none: its waits get this many times the limit.
+constexpr uint64_t kWindowPatience = 64;
+
 // Whether the table's value may vary over a tile of keys [k0, k0 + 128) and
 // rows at positions p0 ... p1: some offset is nearer than the distance.
 __device__ __forceinline__ bool is_near(const ScoreArgs& a, int k0, int p0, int p1) {

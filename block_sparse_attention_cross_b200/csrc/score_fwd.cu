@@ -367,8 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(&c->drain, 0, nullptr, a.spin_ns);
   } else if (warp == kWindow) {
     // ===================== the table's windows ================================
-    // Both slots' next windows, each filled as soon as its buffer is free
-    // (polled, so that no slot waits for the other).
+    // The windows of both slots' tiles near the diagonal, each filled as soon as
+    // its buffer is free (polled, so that no slot waits for the other).
     if ((F & kBias) && a.table != nullptr) {
       Cursor cu[2];
       uint32_t n[2] = {0, 0};
@@ -381,22 +381,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           if (cu[s].done) continue;
-          const uint32_t e = n[s] & 1;
-          if (!__all_sync(0xffffffffu, mbar_test_wait(&c->win_empty[s][e], ((n[s] >> 1) & 1) ^ 1))) continue;
           const Walk& w = cu[s].w;
           const int p0 = a.q_start[w.b] + (a.packed ? 0 : w.qb * TILE), p1 = p0 + (a.packed ? a.Nq : TILE) - 1;
-          if (is_near(a, w.kb * TILE, p0, p1))
+          const uint32_t e = n[s] & 1;
+          if (is_near(a, w.kb * TILE, p0, p1)) {
+            if (!__all_sync(0xffffffffu, mbar_test_wait(&c->win_empty[s][e], ((n[s] >> 1) & 1) ^ 1))) continue;
             fill_window(a, a.packed ? w.hx * a.G : w.hx, a.packed ? a.G : 1, w.kb * TILE - p1,
                         reinterpret_cast<float*>(smem + L::OFF_WIN + s * L::WIN + e * (L::WIN / 2)), nullptr,
                         &c->win_info[s][e], &corrupt);
-          mbar_arrive(&c->win_full[s][e]);
-          ++n[s];
+            mbar_arrive(&c->win_full[s][e]);
+            ++n[s];
+          }
           cursor_next(f, cu[s]);
           moved = true;
         }
         const uint64_t now = globaltimer_ns();
         if (moved) since = now;
-        else ok = __all_sync(0xffffffffu, now - since <= a.spin_ns && *static_cast<volatile int*>(&c->abort) == 0);
+        else __nanosleep(200);   // leave the issue slots to the softmax warps
+        ok = moved || __all_sync(0xffffffffu, now - since <= kWindowPatience * a.spin_ns && *static_cast<volatile int*>(&c->abort) == 0);
       }
       if (!ok) {
         c->abort = 1;
@@ -413,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_o = t_s + 128;
     // Scores are in log2 units.
     const ScoreTerms terms = score_terms(a);
-    uint32_t gb = 0;
+    uint32_t gb = 0, nw = 0;   // key tiles and windows consumed
     int tiles = 0;
     bool ok = true, corrupt = false;
     const int slots = 2 * gridDim.x;
@@ -480,9 +482,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (bool first = true;; first = false, ++gb) {
         const int k0 = w.kb * TILE;
         const bool edge = k0 < tr.z || k0 + TILE > tr.w;
+        const bool near = (F & kBias) && is_near(a, k0, p0, p1);
         bool got = mbar_wait(&c->s_full[slot], gb & 1, &c->abort, a.spin_ns);
-        if ((F & kBias) && got && a.table != nullptr)
-          got = mbar_wait(&c->win_full[slot][gb & 1], (gb >> 1) & 1, &c->abort, a.spin_ns);
+        if (near && got) got = mbar_wait(&c->win_full[slot][nw & 1], (nw >> 1) & 1, &c->abort, a.spin_ns);
         ok = __all_sync(0xffffffffu, got);
         if (!ok) break;
         tc_fence_after();
@@ -512,12 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the ordinary tiles skip cost them (masks inside their loops: plain
         // scores 932 -> 1003 us, capped 1127 -> 1351 us at 24 heads of 8192
         // tokens, d = 128; all 128 columns unrolled: 1573 us capped).
-        const bool near = (F & kBias) && is_near(a, k0, p0, p1);
         ScoreBias bias = {};
         if (F & kBias) {
-          bias.wr = reinterpret_cast<const float*>(smem + L::OFF_WIN + slot * L::WIN + (gb & 1) * (L::WIN / 2)) +
+          bias.wr = reinterpret_cast<const float*>(smem + L::OFF_WIN + slot * L::WIN + (nw & 1) * (L::WIN / 2)) +
                     (a.packed ? min((FEW ? lane : row) / a.Nq, a.G - 1) * 256 : 0) + (p1 - (live ? p : p1));
-          bias.window = near && c->win_info[slot][gb & 1].cuts > 0;
+          bias.window = near && c->win_info[slot][nw & 1].cuts > 0;
           bias.flat = near ? (bias.window ? 0.f : bias.wr[0]) : k0 > p1 ? far_hi : far_lo;
           bias.side = k0 >= p1 ? 1 : k0 + TILE - 1 <= p0 ? -1 : 0;
           bias.slope = slope;
@@ -641,7 +642,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) softmax(IntC<kCutTile>{});
         else if ((F & 3) == kBias && a.slopes == nullptr && !bias.window) softmax(IntC<kFlatTile>{});
         else softmax(IntC<kFullTile>{});
-        if ((F & kBias) && a.table != nullptr) mbar_arrive(&c->win_empty[slot][gb & 1]);
         if (FEW) {   // the other warps' columns are 0 in these lanes
           uint32_t pk[16];
 #pragma unroll
@@ -667,8 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         f2unpack(acc1, b0, b1);
         l = l * alpha + ((a0 + a1) + (b0 + b1));
         tmem_st_wait();
-        } else if ((F & kBias) && a.table != nullptr) {
-          mbar_arrive(&c->win_empty[slot][gb & 1]);
+        }
+        if (near) {
+          mbar_arrive(&c->win_empty[slot][nw & 1]);
+          ++nw;
         }
         tc_fence_before();
         mbar_arrive(&c->p_full[slot]);
