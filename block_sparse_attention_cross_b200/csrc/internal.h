@@ -112,6 +112,7 @@ struct ScoreArgs {
 };
 
 // score_simt.cu (fp32, FFMA)
+int score_splits_simt(int B, int H, int Nq, int Nk);
 int launch_score_fwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_score_bwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 // score_fwd.cu (bf16, tcgen05)
@@ -123,7 +124,8 @@ int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_attn_spans(int B, int Nq, int Nk, int causal, const int32_t* docs, int n_docs, const int32_t* prefix,
                       const int32_t* kv_len, const int32_t* q_len, const int32_t* q_start, int2* row, int4* tile,
                       int32_t* q_start_out, cudaStream_t s);
-// score_rows.cu: per-row terms of the fp32 backward pass, the sum of the table's partial gradients
+// score_rows.cu: the join of partial results, per-row terms of the fp32 backward pass, the sum of the table's partial gradients
+int launch_score_join(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
 int launch_score_rows(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_score_table_sum(const ScoreArgs& a, int dtype, cudaStream_t s);
 

@@ -201,10 +201,14 @@ int calibatt_score_attn_fwd_workspace_size(int B, int H, int Hkv, int Nq, int Nk
   if (bytes == nullptr) return set_error(CALIBATT_E_INVALID, "bytes is NULL");
   if (int rc = check_sizes(B, H, Hkv, Nq, Nk, d, dtype)) return rc;
   *bytes = 0;
-  if (dtype != CALIBATT_BF16) return CALIBATT_OK;
   // enough for every score function and mask of these sizes
   ScoreArgs a{};
   a.B = B; a.H = H; a.Hkv = Hkv; a.G = H / Hkv; a.Nq = Nq; a.nqb = (Nq + 127) / 128; a.nkb = (Nk + 127) / 128;
+  if (dtype == CALIBATT_FP32) {
+    a.splits = a.parts = score_splits_simt(B, H, Nq, Nk);
+    *bytes = fwd_layout(a, d, nullptr);
+    return CALIBATT_OK;
+  }
   for (int packed = 0; packed < 2; ++packed) {
     if (packed && !score_packs(a.G, Nq, false, false)) continue;
     fwd_plan(a, packed != 0);
@@ -231,13 +235,13 @@ int calibatt_score_attn_fwd(const calibatt_tensor4* q, const calibatt_tensor4* k
   a.lse = lse;
   a.status = dev_status;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (dtype == CALIBATT_FP32) return launch_score_fwd_simt(a, d, s);
-  fwd_plan(a, score_packs(a.G, Nq, a.mask != nullptr, a.table != nullptr));
+  if (dtype == CALIBATT_FP32) a.splits = a.parts = score_splits_simt(B, H, Nq, Nk);
+  else fwd_plan(a, score_packs(a.G, Nq, a.mask != nullptr, a.table != nullptr));
   const size_t need = fwd_layout(a, d, workspace);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0))
     return set_error(CALIBATT_E_WORKSPACE, "workspace of %zu bytes (256-byte aligned) needed, %zu given", need,
                      workspace_bytes);
-  return launch_score_fwd_tc(a, d, s);
+  return dtype == CALIBATT_FP32 ? launch_score_fwd_simt(a, d, s) : launch_score_fwd_tc(a, d, s);
 }
 
 int calibatt_score_attn_bwd_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int dtype, int n_buckets,

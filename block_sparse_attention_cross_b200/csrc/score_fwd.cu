@@ -22,8 +22,8 @@
 //  - with at most 32 such rows they are repeated in all four lane quarters of
 //    the tile, and each warp takes a quarter of every key tile's columns (a
 //    warp reaches only its own TMEM lanes), leaving four partial results;
-//  - few tiles against many keys are split along the keys; k_score_join adds
-//    the partial results in a fixed order.
+//  - few tiles against many keys are split along the keys; k_score_join
+//    (score_rows.cu) adds the partial results in a fixed order.
 // Bound: MUFU and tensor core together for long queries (see the figures at
 // the launch), HBM for few queries.
 #include <algorithm>
@@ -742,59 +742,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMma) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Joins the partial results of a row: weights e^(lse_s - max).  One CTA a row;
-// warp w adds up the parts w, w + 4, ... (a lane D / 32 columns), then the
-// warps' sums are added in warp order: a fixed order.  Reads the partial
-// results once.
-template <int D>
-__global__ void __launch_bounds__(128) k_score_join(const ScoreArgs a) {
-  constexpr int C = D / 32;
-  __shared__ float sums[4][D], norm[4];
-  const long long r = blockIdx.x;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const float* pl = a.part_lse + r * a.parts;
-  float mx = -INFINITY;
-  for (int s = lane; s < a.parts; s += 32) mx = fmaxf(mx, pl[s]);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-  float acc[C] = {}, l = 0.f;
-  // eight parts' loads in flight; a part that saw nothing has no partial O
-  for (int s0 = w; s0 < a.parts; s0 += 32) {
-    float x[8], po[8][C];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int s = min(s0 + 4 * k, a.parts - 1);
-      x[k] = s0 + 4 * k < a.parts ? pl[s] : -INFINITY;
-#pragma unroll
-      for (int e = 0; e < C; ++e) po[k][e] = a.part_o[(r * a.parts + s) * D + lane * C + e];
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (x[k] == -INFINITY) continue;
-      const float wgt = expf(x[k] - mx);   // NaN stays NaN
-      l += wgt;
-#pragma unroll
-      for (int e = 0; e < C; ++e) acc[e] = fmaf(wgt, po[k][e], acc[e]);
-    }
-  }
-#pragma unroll
-  for (int e = 0; e < C; ++e) sums[w][lane * C + e] = acc[e];
-  if (lane == 0) norm[w] = l;
-  __syncthreads();
-  l = (norm[0] + norm[1]) + (norm[2] + norm[3]);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int i = static_cast<int>(r % a.Nq);
-  const int bh = static_cast<int>(r / a.Nq), b = bh / a.H, h = bh % a.H;
-  __nv_bfloat16* op = reinterpret_cast<__nv_bfloat16*>(a.o.p) + b * a.o.sb + h * a.o.sh + i * a.o.sn;
-  if (threadIdx.x < D / 2) {
-    const int e = threadIdx.x * 2;
-    const float x = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
-    const float y = (sums[0][e + 1] + sums[1][e + 1]) + (sums[2][e + 1] + sums[3][e + 1]);
-    *reinterpret_cast<uint32_t*>(op + e) = pack_bf16x2(x * inv, y * inv);
-  }
-  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[r] = l == 0.f ? -INFINITY : mx + logf(l);
-}
-
 template <int D, int F>
 int launch(const ScoreArgs& a, int sms, cudaStream_t s) {
   FwdArgs f;
@@ -822,13 +769,7 @@ int launch(const ScoreArgs& a, int sms, cudaStream_t s) {
   kern<<<grid, kThreads, Layout<D>::SMEM, s>>>(tq, tk, tv, f);
   count_launch();
   if ((rc = check_launch("k_score_fwd"))) return rc;
-  if (a.parts > 1) {
-    const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;
-    k_score_join<D><<<static_cast<unsigned>(rows), 128, 0, s>>>(a);
-    count_launch();
-    return check_launch("k_score_join");
-  }
-  return CALIBATT_OK;
+  return a.parts > 1 ? launch_score_join(a, D, CALIBATT_BF16, s) : CALIBATT_OK;
 }
 
 }  // namespace

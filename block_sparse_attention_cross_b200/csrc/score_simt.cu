@@ -11,6 +11,8 @@
 // the backward recomputes the scores in both of its passes (keys outer for dK
 // and dV, queries outer for dQ and the table's gradient), so every gradient is
 // summed by one CTA in a fixed order, without atomics.
+#include <algorithm>
+
 #include "score_common.cuh"
 
 namespace calibatt {
@@ -106,26 +108,50 @@ __device__ __forceinline__ void mul_tile_t(float (&acc)[4][D / 16], const float*
 // of 0 of a masked pair would turn them into NaN.
 template <int D>
 __device__ __forceinline__ void clean_rows(float* X, int* bad) {
-  for (int r = threadIdx.x; r < BT; r += kThreads) {
-    bool ok = true;
-    for (int c = 0; c < D; ++c) ok = ok && isfinite(X[r * PD<D> + c]);
-    if (!ok)
-      for (int c = 0; c < D; ++c) X[r * PD<D> + c] = 0.f;
-    bad[r] = !ok;
+  const int r = threadIdx.x >> 2, part = threadIdx.x & 3;   // four threads a row
+  float* at = X + r * PD<D> + part * (D / 4);
+  bool ok = true;
+#pragma unroll
+  for (int c = 0; c < D / 4; c += 4) {
+    const float4 v = *reinterpret_cast<const float4*>(at + c);
+    ok = ok && isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w);
+  }
+  ok = (__ballot_sync(0xffffffffu, !ok) >> (threadIdx.x & 28) & 15u) == 0;
+  if (!ok) {
+#pragma unroll
+    for (int c = 0; c < D / 4; c += 4) *reinterpret_cast<float4*>(at + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  if (part == 0) bad[r] = !ok;
+}
+
+// The table along the 127 offsets of a 64 x 64 tile: entry x is offset o0 + x.
+// (Read pair by pair from global memory these were the longest part of small
+// training steps.)
+struct Window {
+  float value[2 * BT];
+  int bucket[2 * BT];
+};
+__device__ __forceinline__ void fill_window(const ScoreArgs& a, int h, int o0, Window* w, bool* bad) {
+  if (a.table == nullptr) return;
+  const int x = threadIdx.x;
+  if (x < 2 * BT - 1) {
+    const int n = score_bucket(a, o0 + x, bad);
+    w->bucket[x] = n;
+    w->value[x] = reinterpret_cast<const float*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n];
   }
 }
 
-// z of one pair, and the cap's tanh in *th (0 without a cap).
-__device__ __forceinline__ float score_of(const ScoreArgs& a, int h, float dot, int off, float* th, bool* bad) {
+// z of the pair (row, col) of the tile with offset `off`, and the cap's tanh in *th (0 without a cap).
+__device__ __forceinline__ float score_of(const ScoreArgs& a, float slope, const Window& w, float dot, int row, int col,
+                                          int off, float* th) {
   float z = dot * a.scale;
   *th = 0.f;
   if (a.cap > 0.f) {
     *th = tanhf(z / a.cap);
     z = a.cap * *th;
   }
-  if (a.slopes != nullptr) z -= a.slopes[h] * fabsf(static_cast<float>(off));
-  if (a.table != nullptr)
-    z += reinterpret_cast<const float*>(a.table)[static_cast<size_t>(h) * a.n_buckets + score_bucket(a, off, bad)];
+  if (a.slopes != nullptr) z -= slope * fabsf(static_cast<float>(off));
+  if (a.table != nullptr) z += w.value[col - row + BT - 1];
   return z;
 }
 
@@ -141,11 +167,13 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
   extern __shared__ __align__(16) float sm[];
   float *sQ = sm, *sK = sQ + S::IN, *sV = sK + S::IN, *sP = sV + S::IN;
   __shared__ int bad_row[BT];
+  __shared__ Window win;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int q0 = blockIdx.x * BT, h = blockIdx.y, b = blockIdx.z, hk = h / a.G;
+  const int q0 = blockIdx.x / a.splits * BT, sp = blockIdx.x % a.splits, h = blockIdx.y, b = blockIdx.z, hk = h / a.G;
   const int qb = q0 >> 7;
   const int4 t = score_tile(a, b, qb);
   const int qs = a.q_start[b];
+  const float slope = a.slopes != nullptr ? a.slopes[h] : 0.f;
   int2 vis[4];
   float m[4], l[4], o[4][D / 16];
   bool nan_row[4], bad = false;
@@ -159,12 +187,16 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
     for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
   }
   load_tile<D>(sQ, a.q, b, h, q0, a.Nq);
-  for (int k0 = t.x & ~(BT - 1); k0 < t.y; k0 += BT) {
+  // this split's key tiles
+  const int first = t.x / BT, tiles = max(0, (t.y + BT - 1) / BT - first), per = (tiles + a.splits - 1) / a.splits;
+  const int end = min(t.y, (first + min(tiles, (sp + 1) * per)) * BT);
+  for (int k0 = (first + sp * per) * BT; k0 < end; k0 += BT) {
     if (!score_kept(a, h, qb, k0 >> 7)) continue;
     const bool edge = k0 < t.z || k0 + BT > t.w;
     __syncthreads();
     load_tile<D>(sK, a.k, b, hk, k0, a.Nk);
     load_tile<D>(sV, a.v, b, hk, k0, a.Nk);
+    fill_window(a, h, k0 - (qs + q0) - (BT - 1), &win, &bad);
     __syncthreads();
     if (edge) clean_rows<D>(sV, bad_row);
     float s[4][4] = {};
@@ -178,7 +210,8 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
         const int col = k0 + tx + 16 * j;
         float th;
         const bool see = col >= vis[i].x && col < vis[i].y;
-        s[i][j] = see ? score_of(a, h, s[i][j], col - (qs + q0 + ty * 4 + i), &th, &bad) : -INFINITY;
+        s[i][j] = see ? score_of(a, slope, win, s[i][j], ty * 4 + i, tx + 16 * j, col - (qs + q0 + ty * 4 + i), &th)
+                      : -INFINITY;
         if (edge && see && bad_row[tx + 16 * j]) nan_row[i] = true;
         mx = fmaxf(mx, s[i][j]);
       }
@@ -211,22 +244,32 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
     const int r = q0 + ty * 4 + i;
     if (r >= a.Nq) continue;
     const float inv = (any & 0xffffu) ? NAN : l[i] == 0.f ? 0.f : 1.f / l[i];
+    const float row_lse = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
+    const size_t at = (static_cast<size_t>(b) * a.H + h) * a.Nq + r;
+    if (a.parts > 1) {
+      float* dst = a.part_o + (at * a.parts + sp) * D;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        store4(dst + tx * 4 + 64 * c, o[i][c * 4] * inv, o[i][c * 4 + 1] * inv, o[i][c * 4 + 2] * inv, o[i][c * 4 + 3] * inv);
+      if (tx == 0) a.part_lse[at * a.parts + sp] = row_lse;
+      continue;
+    }
     float* dst = reinterpret_cast<float*>(a.o.p) + b * a.o.sb + h * a.o.sh + r * a.o.sn;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
       store4(dst + tx * 4 + 64 * c, o[i][c * 4] * inv, o[i][c * 4 + 1] * inv, o[i][c * 4 + 2] * inv, o[i][c * 4 + 3] * inv);
     if (tx == 0 && a.lse != nullptr)
-      a.lse[(static_cast<size_t>(b) * a.H + h) * a.Nq + r] = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
+      a.lse[at] = row_lse;
   }
 }
 
 // P and the two forms of dS of one score tile: dZ = P (dP - D) (what the bias
 // gets) and dS = dZ (1 - tanh^2) scale (what the dot product gets).
 template <int D>
-__device__ __forceinline__ void grad_tile(const ScoreArgs& a, int h, int q0, int k0, int qs, const int2 (&vis)[4],
+__device__ __forceinline__ void grad_tile(const ScoreArgs& a, float slope, const Window& win, int q0, int k0, int qs,
+                                          const int2 (&vis)[4],
                                           const float (&lse)[4], const float (&dd)[4], const float (&s)[4][4],
-                                          const float (&dp)[4][4], int ty, int tx, float* sP, float* sZ, float* sS,
-                                          bool* bad) {
+                                          const float (&dp)[4][4], int ty, int tx, float* sP, float* sZ, float* sS) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -234,7 +277,7 @@ __device__ __forceinline__ void grad_tile(const ScoreArgs& a, int h, int q0, int
       const int col = k0 + tx + 16 * j, at = (ty * 4 + i) * PS + tx + 16 * j;
       float th, p = 0.f, dz = 0.f;
       if (col >= vis[i].x && col < vis[i].y) {
-        const float z = score_of(a, h, s[i][j], col - (qs + q0 + ty * 4 + i), &th, bad);
+        const float z = score_of(a, slope, win, s[i][j], ty * 4 + i, tx + 16 * j, col - (qs + q0 + ty * 4 + i), &th);
         p = expf(z - lse[i]);
         dz = p * (dp[i][j] - dd[i]);
       } else {
@@ -254,11 +297,13 @@ __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
   float* diag = sZ + S::SC;        // [2 BT] sums of dZ over the diagonals of a tile
   float* acc_t = diag + 2 * BT;    // [n_buckets]
   __shared__ int bad_row[BT];
+  __shared__ Window win;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int q0 = blockIdx.x * BT, h = blockIdx.y, b = blockIdx.z, hk = h / a.G;
   const int qb = q0 >> 7;
   const int4 t = score_tile(a, b, qb);
   const int qs = a.q_start[b];
+  const float slope = a.slopes != nullptr ? a.slopes[h] : 0.f;
   int2 vis[4];
   float lse[4], dd[4], dq[4][D / 16] = {};
   bool bad = false;
@@ -279,11 +324,12 @@ __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
     __syncthreads();
     load_tile<D>(sK, a.k, b, hk, k0, a.Nk);
     load_tile<D>(sV, a.v, b, hk, k0, a.Nk);
+    fill_window(a, h, k0 - (qs + q0) - (BT - 1), &win, &bad);
     __syncthreads();
     float s[4][4] = {}, dp[4][4] = {};
     dot_tile<D>(s, sQ, sK, ty, tx);
     dot_tile<D>(dp, sO, sV, ty, tx);
-    grad_tile<D>(a, h, q0, k0, qs, vis, lse, dd, s, dp, ty, tx, nullptr, a.dtable ? sZ : nullptr, sS, &bad);
+    grad_tile<D>(a, slope, win, q0, k0, qs, vis, lse, dd, s, dp, ty, tx, nullptr, a.dtable ? sZ : nullptr, sS);
     __syncthreads();
     if (edge) {
       clean_rows<D>(sK, bad_row);   // the scores that read them are formed: a visible one is in dS as NaN
@@ -292,18 +338,21 @@ __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
     mul_tile<D>(dq, sS, sK, ty, tx);
     if (a.dtable != nullptr) {
       // offset j - p of diagonal x: column - row = x - (BT - 1)
-      for (int x = threadIdx.x; x < 2 * BT - 1; x += kThreads) {
-        float v = 0.f;
-        for (int r = max(0, BT - 1 - x); r < BT && r + x - (BT - 1) < BT; ++r) v += sZ[r * PS + r + x - (BT - 1)];
-        diag[x] = v;
+      // (two threads a diagonal: its upper and lower half, added in that order)
+      const int x = threadIdx.x >> 1, low = threadIdx.x & 1;
+      float v = 0.f;
+      if (x < 2 * BT - 1) {
+        const int r0 = max(0, BT - 1 - x), r1 = min(BT, 2 * BT - 1 - x), mid = (r0 + r1) / 2;
+        for (int r = low ? mid : r0; r < (low ? r1 : mid); ++r) v += sZ[r * PS + r + x - (BT - 1)];
       }
+      v += __shfl_xor_sync(0xffffffffu, v, 1);
+      if (x < 2 * BT - 1 && !low) diag[x] = v;
       __syncthreads();
-      const int off0 = k0 - (qs + q0) - (BT - 1);
       for (int n = threadIdx.x; n < a.n_buckets; n += kThreads) {
-        float v = 0.f;
-        for (int x = 0; x < 2 * BT - 1; ++x)
-          if (score_bucket(a, off0 + x, &bad) == n) v += diag[x];
-        acc_t[n] += v;
+        float sum = 0.f;
+#pragma unroll 8
+        for (int d = 0; d < 2 * BT - 1; ++d) sum += win.bucket[d] == n ? diag[d] : 0.f;
+        acc_t[n] += sum;
       }
     }
   }
@@ -330,6 +379,7 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
   extern __shared__ __align__(16) float sm[];
   float *sQ = sm, *sO = sQ + S::IN, *sK = sO + S::IN, *sV = sK + S::IN, *sS = sV + S::IN, *sP = sS + S::SC;
   __shared__ int bad_row[BT];
+  __shared__ Window win;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   const int k0 = blockIdx.x * BT, hk = blockIdx.y, b = blockIdx.z;
   const int qs = a.q_start[b];
@@ -339,6 +389,7 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
   load_tile<D>(sV, a.v, b, hk, k0, a.Nk);
   for (int g = 0; g < a.G; ++g) {
     const int h = hk * a.G + g;
+    const float slope = a.slopes != nullptr ? a.slopes[h] : 0.f;
     for (int q0 = 0; q0 < a.Nq; q0 += BT) {
       const int qb = q0 >> 7;
       const int4 t = score_tile(a, b, qb);
@@ -347,6 +398,7 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
       __syncthreads();
       load_tile<D>(sQ, a.q, b, h, q0, a.Nq);
       load_tile<D>(sO, a.dout, b, h, q0, a.Nq);
+      fill_window(a, h, k0 - (qs + q0) - (BT - 1), &win, &bad);
       int2 vis[4];
       float lse[4], dd[4];
       const size_t r0 = (static_cast<size_t>(b) * a.H + h) * a.nqb * 128 + q0;
@@ -360,7 +412,7 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
       float s[4][4] = {}, dp[4][4] = {};
       dot_tile<D>(s, sQ, sK, ty, tx);
       dot_tile<D>(dp, sO, sV, ty, tx);
-      grad_tile<D>(a, h, q0, k0, qs, vis, lse, dd, s, dp, ty, tx, sP, nullptr, sS, &bad);
+      grad_tile<D>(a, slope, win, q0, k0, qs, vis, lse, dd, s, dp, ty, tx, sP, nullptr, sS);
       __syncthreads();
       if (edge) {
         clean_rows<D>(sQ, bad_row);
@@ -400,9 +452,10 @@ int fwd(const ScoreArgs& a, cudaStream_t s) {
   using S = SimtSmem<D>;
   const size_t smem = (3 * S::IN + S::SC) * sizeof(float);
   if (int rc = set_smem(k_score_fwd_simt<D>, smem)) return rc;
-  k_score_fwd_simt<D><<<dim3((a.Nq + BT - 1) / BT, a.H, a.B), kThreads, smem, s>>>(a);
+  k_score_fwd_simt<D><<<dim3((a.Nq + BT - 1) / BT * a.splits, a.H, a.B), kThreads, smem, s>>>(a);
   count_launch();
-  return check_launch("k_score_fwd_simt");
+  if (int rc = check_launch("k_score_fwd_simt")) return rc;
+  return a.parts > 1 ? launch_score_join(a, D, CALIBATT_FP32, s) : CALIBATT_OK;
 }
 
 template <int D>
@@ -419,6 +472,12 @@ int bwd(const ScoreArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+// Splits of the key axis: two CTAs on each of 148 SMs, at least two key tiles a split.
+int score_splits_simt(int B, int H, int Nq, int Nk) {
+  const long long tiles = static_cast<long long>(B) * H * ((Nq + BT - 1) / BT);
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(296 / tiles, (Nk + BT - 1) / BT / 2)));
+}
 
 int launch_score_fwd_simt(const ScoreArgs& a, int d, cudaStream_t s) { return d == 128 ? fwd<128>(a, s) : fwd<64>(a, s); }
 int launch_score_bwd_simt(const ScoreArgs& a, int d, cudaStream_t s) { return d == 128 ? bwd<128>(a, s) : bwd<64>(a, s); }
