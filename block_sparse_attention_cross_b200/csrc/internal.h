@@ -105,6 +105,8 @@ struct ScoreArgs {
   float* row_lse;           // backward: [B, H, 128 nqb]; fp32: LSE, +inf where a row sees nothing; bf16: -log2(e) of it
   float* row_d;             // backward: [B, H, 128 nqb]; fp32: D; bf16: -D
   int2* row_span;           // backward, bf16: [B, 128 nqb] the rows' intervals, padded to whole tiles
+  int kv_parts;             // backward, bf16: parts of a key tile's query tiles
+  float* part_kv;           // backward, bf16: [kv_parts, 2, B, Hkv, Nk, d] dV and dK
   float* part_table;        // backward: [B, H, table tiles, n_buckets]
   int table_tiles;          // query tiles per head that write part_table
   int32_t* status;
@@ -118,7 +120,8 @@ int launch_score_bwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 // score_fwd.cu (bf16, tcgen05)
 bool score_packs(int G, int Nq, bool mask, bool table);
 int score_splits(int B, int heads, int nq_tiles, bool few, int nkb);
-int launch_score_bwd_tc(const ScoreArgs& a, int d, cudaStream_t s);   // score_bwd.cu
+int score_kv_parts(int B, int Hkv, int G, int nqb, int nkb);   // score_bwd.cu
+int launch_score_bwd_tc(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s);
 // score_plan.cu
 int launch_attn_spans(int B, int Nq, int Nk, int causal, const int32_t* docs, int n_docs, const int32_t* prefix,

@@ -129,8 +129,8 @@ void fwd_plan(ScoreArgs& a, bool packed) {
   a.parts = a.few ? 4 * a.splits : a.splits;
 }
 
-// Backward workspace: [row_lse][row_d][row_span][part_table], 256-byte aligned pieces.
-size_t bwd_layout(ScoreArgs& a, int dtype, void* ws) {
+// Backward workspace: [row_lse][row_d][row_span][part_kv][part_table], 256-byte aligned pieces.
+size_t bwd_layout(ScoreArgs& a, int d, int dtype, void* ws) {
   char* p = static_cast<char*>(ws);
   size_t off = 0;
   const size_t rows = static_cast<size_t>(a.B) * a.H * a.nqb * 128;
@@ -141,6 +141,11 @@ size_t bwd_layout(ScoreArgs& a, int dtype, void* ws) {
   if (dtype == CALIBATT_BF16) {
     a.row_span = reinterpret_cast<int2*>(p + off);
     off += align256(static_cast<size_t>(a.B) * a.nqb * 128 * 8);
+    a.kv_parts = score_kv_parts(a.B, a.Hkv, a.G, a.nqb, a.nkb);
+    if (a.kv_parts > 1) {
+      a.part_kv = reinterpret_cast<float*>(p + off);
+      off += align256(static_cast<size_t>(a.kv_parts) * 2 * a.B * a.Hkv * a.Nk * d * 4);
+    }
   }
   if (a.dtable != nullptr) {
     a.table_tiles = dtype == CALIBATT_BF16 ? a.nqb : (a.Nq + 63) / 64;
@@ -250,9 +255,10 @@ int calibatt_score_attn_bwd_workspace_size(int B, int H, int Hkv, int Nq, int Nk
   if (int rc = check_sizes(B, H, Hkv, Nq, Nk, d, dtype)) return rc;
   if (n_buckets < 0 || n_buckets > kMaxBuckets) return set_error(CALIBATT_E_INVALID, "bad n_buckets %d", n_buckets);
   ScoreArgs a{};
-  a.B = B; a.H = H; a.Nq = Nq; a.nqb = (Nq + 127) / 128; a.n_buckets = n_buckets;
+  a.B = B; a.H = H; a.Hkv = Hkv; a.G = H / Hkv; a.Nq = Nq; a.Nk = Nk;
+  a.nqb = (Nq + 127) / 128; a.nkb = (Nk + 127) / 128; a.n_buckets = n_buckets;
   a.dtable = n_buckets > 0 ? bytes : nullptr;   // only whether it is set matters here
-  *bytes = bwd_layout(a, dtype, nullptr);
+  *bytes = bwd_layout(a, d, dtype, nullptr);
   return CALIBATT_OK;
 }
 
@@ -285,7 +291,7 @@ int calibatt_score_attn_bwd(const calibatt_tensor4* dout, const calibatt_tensor4
   a.lse = const_cast<float*>(lse);
   a.dtable = dtable;
   a.status = dev_status;
-  const size_t need = bwd_layout(a, dtype, workspace);
+  const size_t need = bwd_layout(a, d, dtype, workspace);
   if (workspace == nullptr || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return set_error(CALIBATT_E_WORKSPACE, "workspace of %zu bytes (256-byte aligned) needed, %zu given", need,
                      workspace_bytes);

@@ -96,43 +96,48 @@ struct DkvCtrl {
   int abort;
 };
 
-// Walk over the (query head, query tile) pairs that see key tile kb.
+// Walk over the (query head, query tile) pairs that see key tile kb, of the
+// pairs g nqb + qb in [u0, u1).
 struct QueryWalk {
   int g, qb;
   uint32_t word;
   int wbase;
 };
+struct QueryRange {
+  int b, hk, kb, u0, u1;
+};
 
-__device__ __forceinline__ uint32_t query_word(const ScoreArgs& a, int b, int hk, int kb, int g, int wbase) {
-  const int qb = wbase + lane_id();
+__device__ __forceinline__ uint32_t query_word(const ScoreArgs& a, const QueryRange& q, int g, int wbase) {
+  const int qb = wbase + lane_id(), u = g * a.nqb + qb;
   bool on = false;
-  if (qb < a.nqb) {
-    const int4 r = score_tile(a, b, qb);
-    on = r.x < r.y && r.x < (kb + 1) * TILE && r.y > kb * TILE && score_kept(a, hk * a.G + g, qb, kb);
+  if (qb < a.nqb && u >= q.u0 && u < q.u1) {
+    const int4 r = score_tile(a, q.b, qb);
+    on = r.x < r.y && r.x < (q.kb + 1) * TILE && r.y > q.kb * TILE && score_kept(a, q.hk * a.G + g, qb, q.kb);
   }
   return __ballot_sync(0xffffffffu, on);
 }
 
 // Next pair; false at the end.
-__device__ __forceinline__ bool query_next(const ScoreArgs& a, int b, int hk, int kb, QueryWalk& w) {
+__device__ __forceinline__ bool query_next(const ScoreArgs& a, const QueryRange& q, QueryWalk& w) {
   while (w.word == 0) {
     w.wbase += 32;
     if (w.wbase >= a.nqb) {
       w.wbase = 0;
-      if (++w.g >= a.G) return false;
+      ++w.g;
     }
-    w.word = query_word(a, b, hk, kb, w.g, w.wbase);
+    if (w.g * a.nqb + w.wbase >= q.u1) return false;
+    w.word = query_word(a, q, w.g, w.wbase);
   }
   w.qb = w.wbase + __ffs(w.word) - 1;
   w.word &= w.word - 1;
   return true;
 }
 
-__device__ __forceinline__ bool query_start(const ScoreArgs& a, int b, int hk, int kb, QueryWalk& w) {
-  w.g = 0;
-  w.wbase = -32;
+__device__ __forceinline__ bool query_start(const ScoreArgs& a, const QueryRange& q, QueryWalk& w) {
+  w.g = q.u0 / a.nqb;
+  w.wbase = (q.u0 - w.g * a.nqb) / 32 * 32 - 32;
   w.word = 0;
-  return query_next(a, b, hk, kb, w);
+  return query_next(a, q, w);
 }
 
 // Rounds 64 fp32 values of a lane to bf16 pairs in TMEM columns [t, t + 32).
@@ -193,9 +198,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // key tiles of a head side by side: they read the same Q and dO; under a
   // causal rule the first ones, which most queries see, start first
-  const int kb = blockIdx.x % a.nkb, bh = blockIdx.x / a.nkb;
+  const int part = blockIdx.x % a.kv_parts, tile = blockIdx.x / a.kv_parts;
+  const int kb = tile % a.nkb, bh = tile / a.nkb;
   const int b = bh / a.Hkv, hk = bh % a.Hkv;
   const int k0 = kb * TILE;
+  const long long units = static_cast<long long>(a.G) * a.nqb;
+  const QueryRange range{b, hk, kb, static_cast<int>(units * part / a.kv_parts),
+                         static_cast<int>(units * (part + 1) / a.kv_parts)};
 
   if (threadIdx.x == 0) {
     mbar_init(&c->kv_full, 1);
@@ -233,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) regs_dec<kControlRegs>();
   if (warp == kProducer) {
     QueryWalk w;
-    bool more = query_start(a, b, hk, kb, w), ok = true;
+    bool more = query_start(a, range, w), ok = true;
     const bool any = more;
     uint32_t t = 0;
     const uint64_t pol = l2_policy_evict_last(), pol_kv = l2_policy_evict_first();
@@ -262,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bulk_load_w(rows + 512, a.row_d + r0, 512, &c->ring_full[e]);
       bulk_load_w(rows + 1024, a.row_span + (static_cast<size_t>(b) * a.nqb + w.qb) * TILE, 1024, &c->ring_full[e]);
       ++t;
-      more = query_next(a, b, hk, kb, w);
+      more = query_next(a, range, w);
     }
     if (lane == 0) {
       if (!ok) {
@@ -278,8 +287,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kMma) {
     uint32_t n = 0;
-    for (int g = 0; g < a.G; ++g)
-      for (int w = 0; w < a.nqb; w += 32) n += __popc(query_word(a, b, hk, kb, g, w));
+    for (int g = range.u0 / a.nqb; g * a.nqb < range.u1; ++g)
+      for (int w = 0; w < a.nqb; w += 32) n += __popc(query_word(a, range, g, w));
     constexpr uint32_t IDESC_S = idesc_bf16_f32(TILE, TILE, false);
     constexpr uint32_t IDESC_O = idesc_bf16_f32(TILE, D, true);
     const uint32_t sK = smem_u32(smem + L::OFF_K), sV = smem_u32(smem + L::OFF_V);
@@ -327,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       QueryWalk w;
       bool bad = false, ok = true;
       uint32_t t = 0;
-      for (bool more = query_start(a, b, hk, kb, w); more; more = query_next(a, b, hk, kb, w)) {
+      for (bool more = query_start(a, range, w); more; more = query_next(a, range, w)) {
         const int p0 = a.q_start[b] + w.qb * TILE;
         if (!is_near(a, k0, p0, p0 + TILE - 1)) continue;
         const int e = t & 1;
@@ -357,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     uint32_t t = 0, nw = 0;   // pairs and windows consumed
     QueryWalk w;
-    for (bool more = query_start(a, b, hk, kb, w); more; more = query_next(a, b, hk, kb, w), ++t) {
+    for (bool more = query_start(a, range, w); more; more = query_next(a, range, w), ++t) {
       const int e = t % R, h = hk * a.G + w.g;
       const int p0 = a.q_start[b] + w.qb * TILE;
       const int4 tr = score_tile(a, b, w.qb);
@@ -527,10 +536,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool live = j < a.Nk;
     const Tensor4& ot = half == 0 ? a.dv : a.dk;
     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(ot.p) + b * ot.sb + hk * ot.sh + static_cast<long long>(j) * ot.sn;
+    const uint32_t src = (half == 0 ? tV : tK) + lanes;
+    const float mul = half == 0 ? 1.f : a.scale;
     if (ok && t > 0) {
       ok = __all_sync(0xffffffffu, mbar_wait(&c->o_full, 0, &c->abort, a.spin_ns));
       tc_fence_after();
-      if (ok) store_row<D>((half == 0 ? tV : tK) + lanes, dst, half == 0 ? 1.f : a.scale, live);
+    }
+    if (ok && a.kv_parts > 1) {   // fp32 partial sums, added up by k_score_kv_join
+      float* po = a.part_kv + (((static_cast<size_t>(part) * 2 + half) * a.B + b) * a.Hkv + hk) * a.Nk * D +
+                  static_cast<size_t>(j) * D;
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t r[32];
+        if (t > 0) {
+          tmem_ld32(src + q * 32, r);
+          tmem_ld_wait();
+          reg_fence(r);
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) r[x] = 0;
+        }
+        if (live) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 4)
+            *reinterpret_cast<float4*>(po + q * 32 + x) =
+                make_float4(u2f(r[x]) * mul, u2f(r[x + 1]) * mul, u2f(r[x + 2]) * mul, u2f(r[x + 3]) * mul);
+        }
+      }
+    } else if (ok && t > 0) {
+      store_row<D>(src, dst, mul, live);
     } else if (ok) {
       zero_row<D>(dst, live);
     }
@@ -587,6 +621,32 @@ struct DqCtrl {
 // read, dP(t + 1), and once dS(t) is stored, dQ(t) and S(t + 2): the scores are
 // a tile ahead and dP(t + 1) is formed during the second half of tile t's
 // arithmetic.
+// dK and dV from the parts' fp32 sums, added in part order; a thread four
+// columns of a row.  Reads the parts once.
+template <int D>
+__global__ void __launch_bounds__(256) k_score_kv_join(const ScoreArgs a) {
+  const long long rows = static_cast<long long>(a.B) * a.Hkv * a.Nk;
+  const long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const int which = blockIdx.y;   // 0: dV, 1: dK
+  const long long row = x / (D / 4);
+  const int col = static_cast<int>(x % (D / 4)) * 4;
+  if (row >= rows) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < a.kv_parts; ++p) {
+    const float4 v = *reinterpret_cast<const float4*>(a.part_kv + ((static_cast<long long>(p) * 2 + which) * rows + row) * D + col);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  const Tensor4& ot = which == 0 ? a.dv : a.dk;
+  const int j = static_cast<int>(row % a.Nk);
+  const int bh = static_cast<int>(row / a.Nk), b = bh / a.Hkv, hk = bh % a.Hkv;
+  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(ot.p) + b * ot.sb + hk * ot.sh +
+                            static_cast<long long>(j) * ot.sn + col) =
+      make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+}
+
 // Adds the warp's sum of v to *acc, in a fixed order.
 __device__ __forceinline__ void add_to_bucket(float* acc, float v) {
 #pragma unroll
@@ -1157,7 +1217,7 @@ int launch(const ScoreArgs& a, cudaStream_t s) {
   if ((rc = make_tmap4_bf16(&tk, a.k, a.B, a.Hkv, a.Nk, D, TILE, 1))) return rc;
   if ((rc = make_tmap4_bf16(&tv, a.v, a.B, a.Hkv, a.Nk, D, TILE, 1))) return rc;
   if ((rc = make_tmap4_bf16(&to, a.dout, a.B, a.H, a.Nq, D, TILE, 1))) return rc;
-  const long long nk = static_cast<long long>(a.B) * a.Hkv * a.nkb, nq = static_cast<long long>(a.B) * a.H * a.nqb;
+  const long long nk = static_cast<long long>(a.B) * a.Hkv * a.nkb * a.kv_parts, nq = static_cast<long long>(a.B) * a.H * a.nqb;
   if (nk >= (1ll << 31) || nq >= (1ll << 31)) return set_error(CALIBATT_E_UNSUPPORTED, "too many tiles");
   static std::atomic<bool> done_kv[kMaxDevices], done_q[2][kMaxDevices];
   auto dkv = k_score_dkv<D, F>;
@@ -1170,10 +1230,23 @@ int launch(const ScoreArgs& a, cudaStream_t s) {
   dq<<<static_cast<unsigned>(nq), kThreads, DqLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
   dkv<<<static_cast<unsigned>(nk), kThreads, DkvLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
   count_launch(2);
+  if (a.kv_parts > 1) {
+    const long long quads = static_cast<long long>(a.B) * a.Hkv * a.Nk * (D / 4);
+    k_score_kv_join<D><<<dim3(static_cast<unsigned>((quads + 255) / 256), 2), 256, 0, s>>>(a);
+    count_launch();
+  }
   return check_launch("k_score_bwd");
 }
 
 }  // namespace
+
+// Parts of the (query head, query tile) pairs of a key tile: with fewer key
+// tiles than SMs the pairs are divided, at least two to a part (five query
+// heads on one key head at 1264 tokens, d = 64: 20 CTAs of 50 pairs otherwise).
+int score_kv_parts(int B, int Hkv, int G, int nqb, int nkb) {
+  const long long tiles = static_cast<long long>(B) * Hkv * nkb;
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(148 / tiles, static_cast<long long>(G) * nqb / 2)));
+}
 
 int launch_score_bwd_tc(const ScoreArgs& a, int d, cudaStream_t s) {
   switch ((a.cap > 0.f ? kCap : 0) | (a.slopes != nullptr || a.table != nullptr ? kBias : 0)) {

@@ -6,16 +6,18 @@
 namespace calibatt {
 namespace {
 
-// Joins the partial results of a row: weights e^(lse_s - max).  One CTA a row;
-// warp w adds up the parts w, w + 4, ... (a lane D / 32 columns), then the
-// warps' sums are added in warp order: a fixed order.  Reads the partial
-// results once.
-template <typename T, int D>
+// Joins the partial results of a row: weights e^(lse_s - max), a lane D / 32
+// columns.  WARPS = 4 (many parts): one CTA a row, warp w adds up the parts w,
+// w + 4, ..., then the warps' sums are added in warp order; WARPS = 1 (up to 8
+// parts): a warp a row (a CTA a row took longer than the forward for two parts
+// of 12 640 rows).  A fixed order either way; reads the parts once.
+template <typename T, int D, int WARPS>
 __global__ void __launch_bounds__(128) k_score_join(const ScoreArgs a) {
   constexpr int C = D / 32;
-  __shared__ float sums[4][D], norm[4];
-  const long long r = blockIdx.x;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  __shared__ float sums[WARPS == 4 ? 4 : 1][D], norm[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, w = WARPS == 4 ? warp : 0;
+  const long long r = WARPS == 4 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 4 + warp;
+  if (r >= static_cast<long long>(a.B) * a.H * a.Nq) return;
   const float* pl = a.part_lse + r * a.parts;
   float mx = -INFINITY;
   for (int s = lane; s < a.parts; s += 32) mx = fmaxf(mx, pl[s]);
@@ -23,12 +25,12 @@ __global__ void __launch_bounds__(128) k_score_join(const ScoreArgs a) {
   for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
   float acc[C] = {}, l = 0.f;
   // eight parts' loads in flight; a part that saw nothing has no partial O
-  for (int s0 = w; s0 < a.parts; s0 += 32) {
+  for (int s0 = w; s0 < a.parts; s0 += 8 * WARPS) {
     float x[8], po[8][C];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int s = min(s0 + 4 * k, a.parts - 1);
-      x[k] = s0 + 4 * k < a.parts ? pl[s] : -INFINITY;
+      const int s = min(s0 + WARPS * k, a.parts - 1);
+      x[k] = s0 + WARPS * k < a.parts ? pl[s] : -INFINITY;
 #pragma unroll
       for (int e = 0; e < C; ++e) po[k][e] = a.part_o[(r * a.parts + s) * D + lane * C + e];
     }
@@ -41,23 +43,36 @@ __global__ void __launch_bounds__(128) k_score_join(const ScoreArgs a) {
       for (int e = 0; e < C; ++e) acc[e] = fmaf(wgt, po[k][e], acc[e]);
     }
   }
+  if constexpr (WARPS == 4) {
 #pragma unroll
-  for (int e = 0; e < C; ++e) sums[w][lane * C + e] = acc[e];
-  if (lane == 0) norm[w] = l;
-  __syncthreads();
-  l = (norm[0] + norm[1]) + (norm[2] + norm[3]);
+    for (int e = 0; e < C; ++e) sums[w][lane * C + e] = acc[e];
+    if (lane == 0) norm[w] = l;
+    __syncthreads();
+    if (w != 0) return;
+    l = (norm[0] + norm[1]) + (norm[2] + norm[3]);
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
+      const int at = lane * C + e;
+      acc[e] = (sums[0][at] + sums[1][at]) + (sums[2][at] + sums[3][at]);
+    }
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int i = static_cast<int>(r % a.Nq);
   const int bh = static_cast<int>(r / a.Nq), b = bh / a.H, h = bh % a.H;
-  T* op = reinterpret_cast<T*>(a.o.p) + b * a.o.sb + h * a.o.sh + i * a.o.sn;
-  if (threadIdx.x < D / 2) {
-    const int e = threadIdx.x * 2;
-    const float x = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
-    const float y = (sums[0][e + 1] + sums[1][e + 1]) + (sums[2][e + 1] + sums[3][e + 1]);
-    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(op + e) = pack_bf16x2(x * inv, y * inv);
-    else *reinterpret_cast<float2*>(op + e) = make_float2(x * inv, y * inv);
+  T* op = reinterpret_cast<T*>(a.o.p) + b * a.o.sb + h * a.o.sh + i * a.o.sn + lane * C;
+#pragma unroll
+  for (int e = 0; e < C; e += 2) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(op + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    else *reinterpret_cast<float2*>(op + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
   }
-  if (threadIdx.x == 0 && a.lse != nullptr) a.lse[r] = l == 0.f ? -INFINITY : mx + logf(l);
+  if (lane == 0 && a.lse != nullptr) a.lse[r] = l == 0.f ? -INFINITY : mx + logf(l);
+}
+
+template <typename T, int D>
+void launch_join(const ScoreArgs& a, cudaStream_t s) {
+  const long long rows = static_cast<long long>(a.B) * a.H * a.Nq;   // below 2^31
+  if (a.parts > 8) k_score_join<T, D, 4><<<static_cast<unsigned>(rows), 128, 0, s>>>(a);
+  else k_score_join<T, D, 1><<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(a);
 }
 
 // fp32: D_i = sum over d of dO_i O_i, and the row's LSE as the backward
@@ -120,14 +135,8 @@ __global__ void __launch_bounds__(128) k_score_table_sum(const ScoreArgs a) {
 }  // namespace
 
 int launch_score_join(const ScoreArgs& a, int d, int dtype, cudaStream_t s) {
-  const unsigned rows = static_cast<unsigned>(static_cast<long long>(a.B) * a.H * a.Nq);   // below 2^31
-  if (dtype == CALIBATT_BF16) {
-    if (d == 128) k_score_join<__nv_bfloat16, 128><<<rows, 128, 0, s>>>(a);
-    else k_score_join<__nv_bfloat16, 64><<<rows, 128, 0, s>>>(a);
-  } else {
-    if (d == 128) k_score_join<float, 128><<<rows, 128, 0, s>>>(a);
-    else k_score_join<float, 64><<<rows, 128, 0, s>>>(a);
-  }
+  if (dtype == CALIBATT_BF16) d == 128 ? launch_join<__nv_bfloat16, 128>(a, s) : launch_join<__nv_bfloat16, 64>(a, s);
+  else d == 128 ? launch_join<float, 128>(a, s) : launch_join<float, 64>(a, s);
   count_launch();
   return check_launch("k_score_join");
 }
