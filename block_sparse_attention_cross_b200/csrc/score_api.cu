@@ -88,6 +88,8 @@ int check_score(ScoreArgs& a, int B, int H, int Hkv, int Nq, int Nk, int d, int 
     return set_error(CALIBATT_E_INVALID, "scale must be finite and > 0");
   if (!(sc->cap >= 0.f) || !std::isfinite(sc->cap))
     return set_error(CALIBATT_E_INVALID, "cap must be finite and >= 0 (0: no cap)");
+  if (!std::isfinite(sc->scale * 4.f) || (sc->cap > 0.f && (!std::isfinite(sc->cap * 4.f) || !std::isfinite(4.f * sc->scale / sc->cap))))
+    return set_error(CALIBATT_E_INVALID, "scale, cap and scale / cap must stay below a quarter of the fp32 range");
   if ((sc->table == nullptr) != (sc->buckets == nullptr))
     return set_error(CALIBATT_E_INVALID, "table and buckets come together");
   if (sc->table != nullptr) {
@@ -107,7 +109,7 @@ int check_score(ScoreArgs& a, int B, int H, int Hkv, int Nq, int Nk, int d, int 
   a.row = reinterpret_cast<const int2*>(sp->row);
   a.tile = reinterpret_cast<const int4*>(sp->tile);
   a.q_start = sp->q_start;
-  a.spin_ns = spin_limit_ns();
+  a.spin_ns = std::min<uint64_t>(spin_limit_ns(), 1ull << 57);   // the window warps' waits take a multiple of it
   return CALIBATT_OK;
 }
 

@@ -265,7 +265,8 @@ __device__ __forceinline__ ScoreTerms score_terms(const ScoreArgs& a) {
     const float k = a.scale / a.cap, k2 = k * k;
     t.capA = a.cap * kLog2e;
     t.kcap = 2.f * kLog2e * k;
-    t.small = 0.6f / k;
+    // (the coefficients hold powers of k up to the eighth: only where those stay far inside fp32)
+    t.small = k > 1e-4f && k < 1e3f ? 0.6f / k : -1.f;
     t.inv = 1.f / t.capA;
     // tanh(x) / x as a polynomial in x^2, interpolated at the five Chebyshev
     // nodes of [0, 0.36] (relative error at most 8e-8)

@@ -71,6 +71,8 @@ def _ints(name, x, shape, device):
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.is_cuda and t.device != device:
         raise ValueError(f"{name} must be on {device}")
+    if t.dtype == torch.int64:   # lengths are clamped on the device; a wrapped value would not be
+        t = t.clamp(-(1 << 31), (1 << 31) - 1)
     return t.to(device=device, dtype=torch.int32).contiguous()
 
 

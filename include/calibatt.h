@@ -638,7 +638,7 @@ typedef struct calibatt_spans {
 
 /* The score function. */
 typedef struct calibatt_score {
-  float scale;            /* finite, > 0                                                                        */
+  float scale;            /* > 0; scale and scale / cap finite also times 4                                     */
   float cap;              /* finite, > 0; 0: no cap                                                             */
   const float* slopes;    /* [H] float32 device or NULL                                                         */
   const void* table;      /* [H, n_buckets] of the inputs' type, device, or NULL                                */
@@ -712,7 +712,9 @@ int calibatt_score_attn_fwd(const calibatt_tensor4* q, const calibatt_tensor4* k
 
 /*
  * calibatt_score_attn_bwd -- the gradients of the definition above, given dO
- * and the forward's O and LSE (same spans and score).
+ * and the forward's O and LSE (same spans and score).  CALIBATT_FP32 forms D
+ * from O; CALIBATT_BF16 sums it from P and dP in fp32 instead and does not
+ * read o (O's rounding to bf16 would nearly double the error of dQ).
  *  dout, q, o, dq  [B, H, Nq, d];  k, v, dk, dv  [B, Hkv, Nk, d];  lse [B, H,
  *  Nq] float32 (read);  dtable [H, n_buckets] of `dtype` (written) or NULL
  *  (needs score->table).  The slopes have no gradient.

@@ -10,6 +10,11 @@ relative to the value = 2^-8, for fp32 2^-24; all elementwise, first order):
   2 ez (numerator and normaliser).
 * O: probabilities rounded to u, the normaliser corrected for the largest one
   (at most u more), the result rounded to u.
+* The cap's factor 1 - t^2 with |t| <= 1 rounded to fp32: t is off by at most
+  2^-22 (MUFU exponential and reciprocal, 2 units in the last place each; a
+  rounding of tanhf in fp32), so the factor is off by at most 2 |t| 2^-22 plus
+  a rounding of 1, together below 2^-20, absolutely: where the cap saturates
+  the factor itself is far smaller.  dS gets |dZ| scale 2^-20 from it.
 * D = sum dO O inherits O's error; dZ = P (dP - D); dS rounded to u for its
   product; results rounded to u.  Sums of n terms in fp32 add n 2^-24 of the
   absolute sum, far below u in bf16 and part of ``ez`` in fp32.
@@ -110,7 +115,8 @@ class Case:
                 eD = (np.abs(do[b, h]) * out["o"][b, h]).sum(1, keepdims=True) + d * F24 * (
                     np.abs(do[b, h]) * np.abs(ref["o"][b, h])).sum(1, keepdims=True)
                 edZ = P * (eD + (d + 4) * F24 * adp + (e2 + 4 * F24) * (adp + D))
-                edS = edZ * f + (u + 8 * F24 + e2) * np.abs(ref["dS"][b, h])
+                ef = 2.0 ** -20 * self.scale if self.cap > 0 else 0.0
+                edS = edZ * (f + ef) + (u + 8 * F24 + e2) * np.abs(ref["dS"][b, h]) + ef * np.abs(ref["dZ"][b, h])
                 out["dq"][b, h] = edS @ np.abs(k[b, g]) + (u + Nk * F24) * np.abs(ref["dq"][b, h])
                 out["dk"][b, g] += edS.T @ np.abs(q[b, h])
                 out["dv"][b, g] += (((u + e2) * P).T + Nq * F24 * P.T) @ np.abs(do[b, h])

@@ -213,6 +213,49 @@ def test_caller_buffers_and_refusals():
         cba.score_attn_bwd(q, q, k, v, out, None, sp)
 
 
+def test_lse_is_optional_and_streams_and_sizes_mix():
+    # without an LSE, on another stream, one call after another of other sizes: the same bits
+    side = torch.cuda.Stream()
+    for kw in (dict(Nq=300, H=4, Hkv=2, cap=5.0), dict(Nq=2, Nk=900, H=8, Hkv=2, d=128, causal=True, q_start=[898], buckets=8, distance=90),
+               dict(Nq=70, H=2, slopes=True, dtype=F32)):
+        c = Case(**kw)
+        want = c.run(False)["o"]
+        q, k, v = (c.gpu(x) for x in (c.q, c.k, c.v))
+        sp, skw = c.spans(), c.score_kw()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            o = cba.score_attn_fwd(q, k, v, sp, **skw)
+        side.synchronize()
+        assert torch.equal(o, want)
+
+
+# caps far from the scores on either side (the cap's polynomial is left there)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cap,scale", [(1e-5, 0.125), (1e6, 0.125), (1e5, 4000.0), (60.0, 3.0)])
+def test_caps_of_every_size(dtype, cap, scale):
+    Case(H=1, Nq=150, d=64, dtype=dtype, cap=cap, scale=scale, gain=1e-2 if cap > 1e4 and scale > 1 else 1.0).check()
+
+
+def test_integers_of_any_width_and_place():
+    want = cba.attn_spans(2, 40, 50, causal=True, kv_len=[50, 7], q_start=[10, 0], prefix=[3, 60])
+    got = cba.attn_spans(2, 40, 50, causal=True, kv_len=torch.tensor([1 << 40, 7], device="cuda"),
+                         q_start=torch.tensor([10, 0], dtype=torch.int16), prefix=np.array([[3], [60]]))
+    assert torch.equal(want.row, got.row) and torch.equal(want.tile, got.tile)
+
+
+# a row's bits do not depend on other rows, heads or batch entries
+def test_rows_stand_alone():
+    c = Case(B=2, H=4, Hkv=2, Nq=260, d=128, cap=20.0, buckets=8, distance=40, causal=True)
+    want = c.run(True)
+    c.q[1, 3, 100:] *= 50      # beyond the polynomial's range
+    c.k[1, 1, 230:] *= 30
+    got = c.run(True)
+    for name in ("o", "dq"):
+        assert torch.equal(want[name][0], got[name][0]), name
+        assert torch.equal(want[name][1, :2], got[name][1, :2]), name
+        assert torch.equal(want[name][1, 3, :100], got[name][1, 3, :100]), name
+
+
 def test_fused_projection_views():
     # q, k, v as slices of one [B, N, 3, H, d] projection
     g = torch.Generator().manual_seed(5)
