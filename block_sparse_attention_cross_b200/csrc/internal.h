@@ -105,8 +105,10 @@ struct ScoreArgs {
   float* row_lse;           // backward: [B, H, 128 nqb]; fp32: LSE, +inf where a row sees nothing; bf16: -log2(e) of it
   float* row_d;             // backward: [B, H, 128 nqb]; fp32: D; bf16: -D
   int2* row_span;           // backward, bf16: [B, 128 nqb] the rows' intervals, padded to whole tiles
-  int kv_parts;             // backward, bf16: parts of a key tile's query tiles
-  float* part_kv;           // backward, bf16: [kv_parts, 2, B, Hkv, Nk, d] dV and dK
+  int kv_parts;             // backward: parts of a key tile's query tiles
+  float* part_kv;           // backward: [kv_parts, 2, B, Hkv, Nk, d] dV and dK
+  int q_parts;              // backward, fp32: parts of a query tile's key tiles
+  float* part_q;            // backward, fp32: [q_parts, B, H, Nq, d] dQ
   float* part_table;        // backward: [B, H, table tiles, n_buckets]
   int table_tiles;          // query tiles per head that write part_table
   int32_t* status;
@@ -115,6 +117,8 @@ struct ScoreArgs {
 
 // score_simt.cu (fp32, FFMA)
 int score_splits_simt(int B, int H, int Nq, int Nk);
+int score_q_parts_simt(int B, int H, int Nq, int Nk);
+int score_kv_parts_simt(int B, int Hkv, int G, int Nq, int Nk);
 int launch_score_fwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_score_bwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 // score_fwd.cu (bf16, tcgen05)
@@ -129,6 +133,7 @@ int launch_attn_spans(int B, int Nq, int Nk, int causal, const int32_t* docs, in
                       int32_t* q_start_out, cudaStream_t s);
 // score_rows.cu: the join of partial results, per-row terms of the fp32 backward pass, the sum of the table's partial gradients
 int launch_score_join(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
+int launch_score_sum_parts(const ScoreArgs& a, int d, int dtype, cudaStream_t s);
 int launch_score_rows(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_score_table_sum(const ScoreArgs& a, int dtype, cudaStream_t s);
 

@@ -131,7 +131,7 @@ void fwd_plan(ScoreArgs& a, bool packed) {
   a.parts = a.few ? 4 * a.splits : a.splits;
 }
 
-// Backward workspace: [row_lse][row_d][row_span][part_kv][part_table], 256-byte aligned pieces.
+// Backward workspace: [row_lse][row_d][row_span][part_kv][part_q][part_table], 256-byte aligned pieces.
 size_t bwd_layout(ScoreArgs& a, int d, int dtype, void* ws) {
   char* p = static_cast<char*>(ws);
   size_t off = 0;
@@ -144,13 +144,21 @@ size_t bwd_layout(ScoreArgs& a, int d, int dtype, void* ws) {
     a.row_span = reinterpret_cast<int2*>(p + off);
     off += align256(static_cast<size_t>(a.B) * a.nqb * 128 * 8);
     a.kv_parts = score_kv_parts(a.B, a.Hkv, a.G, a.nqb, a.nkb);
-    if (a.kv_parts > 1) {
-      a.part_kv = reinterpret_cast<float*>(p + off);
-      off += align256(static_cast<size_t>(a.kv_parts) * 2 * a.B * a.Hkv * a.Nk * d * 4);
-    }
+    a.q_parts = 1;
+  } else {
+    a.kv_parts = score_kv_parts_simt(a.B, a.Hkv, a.G, a.Nq, a.Nk);
+    a.q_parts = score_q_parts_simt(a.B, a.H, a.Nq, a.Nk);
+  }
+  if (a.kv_parts > 1) {
+    a.part_kv = reinterpret_cast<float*>(p + off);
+    off += align256(static_cast<size_t>(a.kv_parts) * 2 * a.B * a.Hkv * a.Nk * d * 4);
+  }
+  if (a.q_parts > 1) {
+    a.part_q = reinterpret_cast<float*>(p + off);
+    off += align256(static_cast<size_t>(a.q_parts) * a.B * a.H * a.Nq * d * 4);
   }
   if (a.dtable != nullptr) {
-    a.table_tiles = dtype == CALIBATT_BF16 ? a.nqb : (a.Nq + 63) / 64;
+    a.table_tiles = dtype == CALIBATT_BF16 ? a.nqb : (a.Nq + 63) / 64 * a.q_parts;
     a.part_table = reinterpret_cast<float*>(p + off);
     off += align256(static_cast<size_t>(a.B) * a.H * a.table_tiles * a.n_buckets * 4);
   }

@@ -542,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(&c->o_full, 0, &c->abort, a.spin_ns));
       tc_fence_after();
     }
-    if (ok && a.kv_parts > 1) {   // fp32 partial sums, added up by k_score_kv_join
+    if (ok && a.kv_parts > 1) {   // fp32 partial sums, added up by k_score_sum_parts
       float* po = a.part_kv + (((static_cast<size_t>(part) * 2 + half) * a.B + b) * a.Hkv + hk) * a.Nk * D +
                   static_cast<size_t>(j) * D;
 #pragma unroll 1
@@ -621,32 +621,6 @@ struct DqCtrl {
 // read, dP(t + 1), and once dS(t) is stored, dQ(t) and S(t + 2): the scores are
 // a tile ahead and dP(t + 1) is formed during the second half of tile t's
 // arithmetic.
-// dK and dV from the parts' fp32 sums, added in part order; a thread four
-// columns of a row.  Reads the parts once.
-template <int D>
-__global__ void __launch_bounds__(256) k_score_kv_join(const ScoreArgs a) {
-  const long long rows = static_cast<long long>(a.B) * a.Hkv * a.Nk;
-  const long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  const int which = blockIdx.y;   // 0: dV, 1: dK
-  const long long row = x / (D / 4);
-  const int col = static_cast<int>(x % (D / 4)) * 4;
-  if (row >= rows) return;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int p = 0; p < a.kv_parts; ++p) {
-    const float4 v = *reinterpret_cast<const float4*>(a.part_kv + ((static_cast<long long>(p) * 2 + which) * rows + row) * D + col);
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
-  }
-  const Tensor4& ot = which == 0 ? a.dv : a.dk;
-  const int j = static_cast<int>(row % a.Nk);
-  const int bh = static_cast<int>(row / a.Nk), b = bh / a.Hkv, hk = bh % a.Hkv;
-  *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(ot.p) + b * ot.sb + hk * ot.sh +
-                            static_cast<long long>(j) * ot.sn + col) =
-      make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-}
-
 // Adds the warp's sum of v to *acc, in a fixed order.
 __device__ __forceinline__ void add_to_bucket(float* acc, float v) {
 #pragma unroll
@@ -1230,12 +1204,8 @@ int launch(const ScoreArgs& a, cudaStream_t s) {
   dq<<<static_cast<unsigned>(nq), kThreads, DqLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
   dkv<<<static_cast<unsigned>(nk), kThreads, DkvLayout<D>::SMEM, s>>>(tq, tk, tv, to, a);
   count_launch(2);
-  if (a.kv_parts > 1) {
-    const long long quads = static_cast<long long>(a.B) * a.Hkv * a.Nk * (D / 4);
-    k_score_kv_join<D><<<dim3(static_cast<unsigned>((quads + 255) / 256), 2), 256, 0, s>>>(a);
-    count_launch();
-  }
-  return check_launch("k_score_bwd");
+  if (int rc2 = check_launch("k_score_bwd")) return rc2;
+  return launch_score_sum_parts(a, D, CALIBATT_BF16, s);
 }
 
 }  // namespace

@@ -784,13 +784,13 @@ bool score_packs(int G, int Nq, bool mask, bool table) {
 // (query tile and split) at a time.  Units of equal length fill whole rounds
 // of the slots when there are floor(296 rounds / tiles) splits of each tile.
 // Tiles of few rows (serving) write little per split and their sequences
-// differ in length, so they take four rounds of at least four key tiles a
+// differ in length, so they take four rounds, at least two key tiles a
 // split; full tiles write 512 bytes of partial sums per row and split, so they
 // are split into one round, and only when they leave half of the slots idle.
 int score_splits(int B, int heads, int nq_tiles, bool few, int nkb) {
   const long long tiles = static_cast<long long>(B) * heads * nq_tiles;
   const long long want = (few ? 4 : 1) * 296 / tiles;
-  return static_cast<int>(std::max<long long>(1, std::min<long long>(want, nkb / 4)));
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(want, nkb / 2)));
 }
 
 int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s) {

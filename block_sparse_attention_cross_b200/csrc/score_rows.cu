@@ -1,6 +1,6 @@
 // score_rows.cu -- the small kernels around the score-modified attention: the
-// join of the forward's key splits, the fp32 backward's row terms, the sum of
-// the table's gradient.
+// join of the forward's key splits, the sums of the backward's parts, the fp32
+// backward's row terms, the sum of the table's gradient.
 #include "score_common.cuh"
 
 namespace calibatt {
@@ -106,6 +106,48 @@ __global__ void __launch_bounds__(256) k_score_rows(const ScoreArgs a) {
   }
 }
 
+// A gradient from its parts' fp32 sums [parts, B, heads, N, d], added in part
+// order; a thread four columns of a row.  Reads the parts once.
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+    k_score_sum_parts(const float* part, int parts, long long stride, Tensor4 out, int B, int heads, int N) {
+  const long long x = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const long long row = x / (D / 4);
+  const int col = static_cast<int>(x % (D / 4)) * 4;
+  if (row >= static_cast<long long>(B) * heads * N) return;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int p = 0; p < parts; ++p) {
+    const float4 v = *reinterpret_cast<const float4*>(part + p * stride + row * D + col);
+    s.x += v.x;
+    s.y += v.y;
+    s.z += v.z;
+    s.w += v.w;
+  }
+  const int j = static_cast<int>(row % N);
+  const int bh = static_cast<int>(row / N), b = bh / heads, h = bh % heads;
+  T* dst = reinterpret_cast<T*>(out.p) + b * out.sb + h * out.sh + static_cast<long long>(j) * out.sn + col;
+  if constexpr (sizeof(T) == 2) *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+  else *reinterpret_cast<float4*>(dst) = s;
+}
+
+template <typename T, int D>
+void sum_parts(const float* part, int parts, long long stride, const Tensor4& out, int B, int heads, int N, cudaStream_t s) {
+  const long long quads = static_cast<long long>(B) * heads * N * (D / 4);
+  k_score_sum_parts<T, D><<<static_cast<unsigned>((quads + 255) / 256), 256, 0, s>>>(part, parts, stride, out, B, heads, N);
+  count_launch();
+}
+
+template <typename T, int D>
+void sum_all(const ScoreArgs& a, cudaStream_t s) {
+  if (a.q_parts > 1)
+    sum_parts<T, D>(a.part_q, a.q_parts, static_cast<long long>(a.B) * a.H * a.Nq * D, a.dq, a.B, a.H, a.Nq, s);
+  if (a.kv_parts > 1) {
+    const long long one = static_cast<long long>(a.B) * a.Hkv * a.Nk * D;   // [parts, 2 (dV, dK), ...]
+    sum_parts<T, D>(a.part_kv, a.kv_parts, 2 * one, a.dv, a.B, a.Hkv, a.Nk, s);
+    sum_parts<T, D>(a.part_kv + one, a.kv_parts, 2 * one, a.dk, a.B, a.Hkv, a.Nk, s);
+  }
+}
+
 // Gradient of the bias table: the partial sums of every (batch entry, query
 // tile) of a head, added in a fixed order in double.  One CTA per (head,
 // bucket).
@@ -139,6 +181,12 @@ int launch_score_join(const ScoreArgs& a, int d, int dtype, cudaStream_t s) {
   else d == 128 ? launch_join<float, 128>(a, s) : launch_join<float, 64>(a, s);
   count_launch();
   return check_launch("k_score_join");
+}
+
+int launch_score_sum_parts(const ScoreArgs& a, int d, int dtype, cudaStream_t s) {
+  if (dtype == CALIBATT_BF16) d == 128 ? sum_all<__nv_bfloat16, 128>(a, s) : sum_all<__nv_bfloat16, 64>(a, s);
+  else d == 128 ? sum_all<float, 128>(a, s) : sum_all<float, 64>(a, s);
+  return check_launch("k_score_sum_parts");
 }
 
 int launch_score_rows(const ScoreArgs& a, int d, cudaStream_t s) {

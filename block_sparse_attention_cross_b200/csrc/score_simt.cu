@@ -10,7 +10,8 @@
 // together.  Softmax over one pass of the keys with running maximum and sum;
 // the backward recomputes the scores in both of its passes (keys outer for dK
 // and dV, queries outer for dQ and the table's gradient), so every gradient is
-// summed by one CTA in a fixed order, without atomics.
+// summed in a fixed order, without atomics; with few tiles the walks are
+// divided into parts, whose sums are added in part order.
 #include <algorithm>
 
 #include "score_common.cuh"
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
   __shared__ int bad_row[BT];
   __shared__ Window win;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int q0 = blockIdx.x * BT, h = blockIdx.y, b = blockIdx.z, hk = h / a.G;
+  const int q0 = blockIdx.x / a.q_parts * BT, part = blockIdx.x % a.q_parts, h = blockIdx.y, b = blockIdx.z, hk = h / a.G;
   const int qb = q0 >> 7;
   const int4 t = score_tile(a, b, qb);
   const int qs = a.q_start[b];
@@ -318,7 +319,10 @@ __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
     for (int n = threadIdx.x; n < a.n_buckets; n += kThreads) acc_t[n] = 0.f;
   load_tile<D>(sQ, a.q, b, h, q0, a.Nq);
   load_tile<D>(sO, a.dout, b, h, q0, a.Nq);
-  for (int k0 = t.x & ~(BT - 1); k0 < t.y; k0 += BT) {
+  // this part's key tiles
+  const int first = t.x / BT, tiles = max(0, (t.y + BT - 1) / BT - first), per = (tiles + a.q_parts - 1) / a.q_parts;
+  const int end = min(t.y, (first + min(tiles, (part + 1) * per)) * BT);
+  for (int k0 = (first + part * per) * BT; k0 < end; k0 += BT) {
     if (!score_kept(a, h, qb, k0 >> 7)) continue;
     const bool edge = k0 < t.z || k0 + BT > t.w;
     __syncthreads();
@@ -361,7 +365,8 @@ __global__ void __launch_bounds__(kThreads) k_score_dq_simt(const ScoreArgs a) {
   for (int i = 0; i < 4; ++i) {
     const int r = q0 + ty * 4 + i;
     if (r >= a.Nq) continue;
-    float* dst = reinterpret_cast<float*>(a.dq.p) + b * a.dq.sb + h * a.dq.sh + r * a.dq.sn;
+    float* dst = a.q_parts > 1 ? a.part_q + (((static_cast<size_t>(part) * a.B + b) * a.H + h) * a.Nq + r) * D
+                               : reinterpret_cast<float*>(a.dq.p) + b * a.dq.sb + h * a.dq.sh + r * a.dq.sn;
 #pragma unroll
     for (int c = 0; c < D / 64; ++c)
       store4(dst + tx * 4 + 64 * c, dq[i][c * 4], dq[i][c * 4 + 1], dq[i][c * 4 + 2], dq[i][c * 4 + 3]);
@@ -381,16 +386,20 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
   __shared__ int bad_row[BT];
   __shared__ Window win;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  const int k0 = blockIdx.x * BT, hk = blockIdx.y, b = blockIdx.z;
+  const int k0 = blockIdx.x / a.kv_parts * BT, part = blockIdx.x % a.kv_parts, hk = blockIdx.y, b = blockIdx.z;
   const int qs = a.q_start[b];
   float dk[4][D / 16] = {}, dv[4][D / 16] = {};
   bool bad = false;
   load_tile<D>(sK, a.k, b, hk, k0, a.Nk);
   load_tile<D>(sV, a.v, b, hk, k0, a.Nk);
-  for (int g = 0; g < a.G; ++g) {
+  // this part's (query head, query tile) pairs g nqt + q0 / 64
+  const int nqt = (a.Nq + BT - 1) / BT;
+  const long long units = static_cast<long long>(a.G) * nqt;
+  const int u0 = static_cast<int>(units * part / a.kv_parts), u1 = static_cast<int>(units * (part + 1) / a.kv_parts);
+  for (int g = u0 / nqt; g < a.G && g * nqt < u1; ++g) {
     const int h = hk * a.G + g;
     const float slope = a.slopes != nullptr ? a.slopes[h] : 0.f;
-    for (int q0 = 0; q0 < a.Nq; q0 += BT) {
+    for (int q0 = max(0, u0 - g * nqt) * BT; q0 < a.Nq && g * nqt + q0 / BT < u1; q0 += BT) {
       const int qb = q0 >> 7;
       const int4 t = score_tile(a, b, qb);
       if (t.x >= k0 + BT || t.y <= k0 || !score_kept(a, h, qb, k0 >> 7)) continue;
@@ -430,6 +439,11 @@ __global__ void __launch_bounds__(kThreads) k_score_dkv_simt(const ScoreArgs a) 
     if (r >= a.Nk) continue;
     float* pk = reinterpret_cast<float*>(a.dk.p) + b * a.dk.sb + hk * a.dk.sh + r * a.dk.sn;
     float* pv = reinterpret_cast<float*>(a.dv.p) + b * a.dv.sb + hk * a.dv.sh + r * a.dv.sn;
+    if (a.kv_parts > 1) {
+      const size_t one = static_cast<size_t>(a.B) * a.Hkv * a.Nk * D;
+      pv = a.part_kv + 2 * part * one + ((static_cast<size_t>(b) * a.Hkv + hk) * a.Nk + r) * D;
+      pk = pv + one;
+    }
 #pragma unroll
     for (int c = 0; c < D / 64; ++c) {
       store4(pk + tx * 4 + 64 * c, dk[i][c * 4], dk[i][c * 4 + 1], dk[i][c * 4 + 2], dk[i][c * 4 + 3]);
@@ -465,18 +479,30 @@ int bwd(const ScoreArgs& a, cudaStream_t s) {
   const size_t smem_k = (4 * S::IN + 2 * S::SC) * sizeof(float);
   if (int rc = set_smem(k_score_dq_simt<D>, smem_q)) return rc;
   if (int rc = set_smem(k_score_dkv_simt<D>, smem_k)) return rc;
-  k_score_dq_simt<D><<<dim3((a.Nq + BT - 1) / BT, a.H, a.B), kThreads, smem_q, s>>>(a);
-  k_score_dkv_simt<D><<<dim3((a.Nk + BT - 1) / BT, a.Hkv, a.B), kThreads, smem_k, s>>>(a);
+  k_score_dq_simt<D><<<dim3((a.Nq + BT - 1) / BT * a.q_parts, a.H, a.B), kThreads, smem_q, s>>>(a);
+  k_score_dkv_simt<D><<<dim3((a.Nk + BT - 1) / BT * a.kv_parts, a.Hkv, a.B), kThreads, smem_k, s>>>(a);
   count_launch(2);
-  return check_launch("k_score_bwd_simt");
+  if (int rc = check_launch("k_score_bwd_simt")) return rc;
+  return launch_score_sum_parts(a, D, CALIBATT_FP32, s);
 }
 
 }  // namespace
 
-// Splits of the key axis: two CTAs on each of 148 SMs, at least two key tiles a split.
+// Splits of the key axis: two CTAs on each of 148 SMs, at least one key tile a split.
 int score_splits_simt(int B, int H, int Nq, int Nk) {
   const long long tiles = static_cast<long long>(B) * H * ((Nq + BT - 1) / BT);
-  return static_cast<int>(std::max<long long>(1, std::min<long long>(296 / tiles, (Nk + BT - 1) / BT / 2)));
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(296 / tiles, (Nk + BT - 1) / BT)));
+}
+
+// Parts of the backward's walks: one CTA (by its shared memory) on each of 148
+// SMs, at least one tile a part.
+int score_q_parts_simt(int B, int H, int Nq, int Nk) {
+  const long long tiles = static_cast<long long>(B) * H * ((Nq + BT - 1) / BT);
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(148 / tiles, (Nk + BT - 1) / BT)));
+}
+int score_kv_parts_simt(int B, int Hkv, int G, int Nq, int Nk) {
+  const long long tiles = static_cast<long long>(B) * Hkv * ((Nk + BT - 1) / BT);
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(148 / tiles, static_cast<long long>(G) * ((Nq + BT - 1) / BT))));
 }
 
 int launch_score_fwd_simt(const ScoreArgs& a, int d, cudaStream_t s) { return d == 128 ? fwd<128>(a, s) : fwd<64>(a, s); }
