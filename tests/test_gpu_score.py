@@ -243,6 +243,64 @@ def test_integers_of_any_width_and_place():
     assert torch.equal(want.row, got.row) and torch.equal(want.tile, got.tile)
 
 
+def test_calls_on_two_streams_at_once():
+    cases = [Case(B=2, H=4, Hkv=2, Nq=700, d=128, cap=9.0, buckets=16, distance=60, causal=True),
+             Case(B=1, H=6, Hkv=2, Nq=3, Nk=3000, slopes=True)]
+    want = [c.run(c.sizes[3] > 3) for c in cases]
+    data = [([c.gpu(x) for x in (c.q, c.k, c.v, c.do)], c.spans(), c.score_kw()) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            (q, k, v, do), sp, kw = data[i]
+            with torch.cuda.stream(st):
+                o, lse = cba.score_attn_fwd(q, k, v, sp, return_lse=True, **kw)
+                got[i].append([o, lse])
+                if i == 0:
+                    got[i][-1] += cba.score_attn_bwd(do, q, k, v, o, lse, sp, **kw)
+    torch.cuda.synchronize()
+    for i in range(2):
+        for run in got[i]:
+            for name, x in zip(("o", "lse", "dq", "dk", "dv", "dtable"), run):
+                assert torch.equal(x, want[i][name]), name
+
+
+def test_map_offset_picks_the_heads_masks():
+    rng = np.random.default_rng(3)
+    maps = torch.from_numpy((rng.random((7, 3, 3)) < 0.6).astype(np.uint8))
+    c = Case(H=2, Nq=300, mask=maps[4:6].contiguous(), cap=7.0)
+    want = c.run(True)
+    q, k, v, do = (c.gpu(x) for x in (c.q, c.k, c.v, c.do))
+    sp, kw = c.spans(), {**c.score_kw(), "mask": maps.cuda(), "map_offset": 4}
+    o, lse = cba.score_attn_fwd(q, k, v, sp, return_lse=True, **kw)
+    g = cba.score_attn_bwd(do, q, k, v, o, lse, sp, **kw)
+    for name, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *g)):
+        assert torch.equal(x, want[name]), name
+
+
+# a cache of 2^31 elements a tensor: all keys and values 0 but the last 40 of the last head
+def test_offsets_beyond_32_bits():
+    H, Nk, d, tail = 8, (1 << 21) + 77, 128, 40
+    g = torch.Generator().manual_seed(1)
+    k = torch.zeros(1, H, Nk, d, dtype=BF, device="cuda")
+    v = torch.zeros_like(k)
+    kt, vt = torch.randn(tail, d, generator=g).to(BF), torch.randn(tail, d, generator=g).to(BF)
+    k[0, -1, -tail:], v[0, -1, -tail:] = kt.cuda(), vt.cuda()
+    q = (torch.randn(1, H, 2, d, generator=g) * 4).to(BF)
+    o, lse = cba.score_attn_fwd(q.cuda(), k, v, cba.attn_spans(1, 2, Nk), scale=0.25, return_lse=True)
+    e = torch.exp(0.25 * q[0, -1].double() @ kt.double().T)          # every other key: exp(0) and a value of 0
+    norm = e.sum(1) + (Nk - tail)
+    want = (e @ vt.double()) / norm[:, None]
+    # probabilities, normaliser and result rounded to bf16 (2^-8 each); the fp32 sum of 2^21 terms of 1 in
+    # 128 x 16384 partial sums is off by at most 2^-24 x 2^14
+    bound = 4 * 2.0 ** -8 * ((e @ vt.double().abs()) / norm[:, None])
+    assert ((o[0, -1].double().cpu() - want).abs() <= bound).all()
+    assert torch.allclose(lse[0, -1].double().cpu(), norm.log(), rtol=0, atol=2.0 ** -9)
+    assert (o[0, :-1] == 0).all() and torch.allclose(lse[0, :-1].double().cpu(), torch.tensor(float(Nk)).double().log(), rtol=0,
+                                                     atol=2.0 ** -9)
+
+
 # a row's bits do not depend on other rows, heads or batch entries
 def test_rows_stand_alone():
     c = Case(B=2, H=4, Hkv=2, Nq=260, d=128, cap=20.0, buckets=8, distance=40, causal=True)
