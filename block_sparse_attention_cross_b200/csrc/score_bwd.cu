@@ -32,7 +32,7 @@
 // sweep at least, against 1024 (first sweep), 1536 and 2048 (dK/dV) tensor
 // cycles at d = 128.  24 heads of 8192 tokens, d = 128: dQ 1.71 ms, dK/dV 1.30
 // ms, together 0.5 PFLOP/s of the products that the gradients need and 0.9 of
-// those that run; with a cap 2.35 and 1.90.  The tensor pipe is 38% busy
+// those that run; with a cap 2.29 and 1.77.  The tensor pipe is 38% busy
 // (capped), the issue slots 40%; the rest is the latency of dependent
 // instructions (1.8 stalled warps an issue).
 #include <algorithm>
@@ -445,14 +445,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
         reg_fence(r);
         float pf[64];   // first the cap's factor, then P times it
-        if (F != 0) {
-          score_columns<F, -1, true, CUT>(a, terms, r, pf, bias, CUT && edge ? kExact : kByScore);
-          if (near) mbar_arrive(&c->win_empty[nw & 1]);
-        }
-        // P, rounded to bf16 for dV, and P times the cap's factor kept for dS
+        // P, rounded to bf16 for dV, and P times the cap's factor kept for dS.
+        // Half of the columns at a time: the two warps of a sub-partition then
+        // alternate between the FMA and the MUFU pipe.
 #pragma unroll
         for (int c32 = 0; c32 < 2; ++c32) {
           const uint32_t seen = c32 ? seen1 : seen0;
+          if (F != 0) {
+            ScoreBias at = bias;
+            at.off0 -= static_cast<float>(32 * c32);
+            at.wr -= 32 * c32;
+            score_columns<F, -1, true, CUT>(a, terms, *reinterpret_cast<uint32_t(*)[32]>(&r[c32 * 32]),
+                                            *reinterpret_cast<float(*)[32]>(&pf[c32 * 32]), at,
+                                            CUT && edge ? kExact : kByScore);
+            if (c32 == 1 && near) mbar_arrive(&c->win_empty[nw & 1]);
+          }
           float pv[32];
           float4 ahead[8];
           if (c32 == 0) {

@@ -31,7 +31,7 @@
 // alone on its sub-partition, runs at its latencies: 2300 cycles of softmax a
 // pair for plain scores, 3300 capped or with slopes, 5100 with both, beside
 // 1660 of products.  24 heads of 8192 tokens, d = 128: 0.91 ms plain (907
-// TFLOP/s), 1.14 capped, 1.16 with slopes, 1.08 with a table.  (Two warpgroups
+// TFLOP/s), 1.14 capped, 1.13 with slopes, 1.04 with a table.  (Two warpgroups
 // a slot, half of the columns each: capped 1.10, but plain 0.96, a table 1.30
 // ms.)  Few queries: HBM; 32 sequences of up to 8191 keys read 670 MB in 0.16
 // ms (4.2 TB/s, 65% of the measured copy).
@@ -180,8 +180,9 @@ constexpr int kBounded = 4;
 // that neither form carries the other's code).
 constexpr int kFew = 8;
 // Key tiles whose scores the mask leaves whole; that it cuts (or where the
-// distance passes 0); and whole ones with one table value and no other term.
-enum TileKind { kFullTile, kCutTile, kFlatTile };
+// distance passes 0); and, without a cap, whole ones with one table value and
+// no slope, or with a slope and one table value.
+enum TileKind { kFullTile, kCutTile, kFlatTile, kLinearTile };
 // Largest cap in log2 units that goes without a maximum: probabilities
 // 2^score lie in 2^+-80, their sums over 2^24 keys and their products with V
 // (|v| < 2^20) inside fp32, and bf16 has fp32's exponents.
@@ -538,12 +539,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t acc0 = f2pack(0.f, 0.f), acc1 = acc0;
         auto softmax = [&](auto cut_c) {
           constexpr bool CUT = decltype(cut_c)::value == kCutTile;
-          // raw scores in both passes: no terms, or one table value for the whole tile
-          constexpr bool RAW = (F & 3) == 0 || decltype(cut_c)::value == kFlatTile;
+          // raw scores in both passes: no terms, one table value for the whole
+          // tile, or a distance that is linear over it (per column slope x,
+          // added in the scale's FFMA, and a constant per chunk)
+          constexpr bool LINEAR = decltype(cut_c)::value == kLinearTile;
+          constexpr bool RAW = (F & 3) == 0 || decltype(cut_c)::value == kFlatTile || LINEAR;
           // columns of a chunk: 64 where the code is short (plain 904 against 925
           // us), else 32 (capped 1137 against 1207 us, a table 1199 against 1342)
-          constexpr int W = RAW && !CUT && !FEW ? 64 : 32;
+          constexpr int W = RAW && !LINEAR && !CUT && !FEW ? 64 : 32;
           const float scale = RAW ? terms.sc : 1.f, offset = RAW && (F & 3) ? bias.flat : 0.f;
+          const float sl = bias.side > 0 ? -slope : slope;   // LINEAR: the distance's part is sl (off0 + x)
+          const uint64_t sc2 = f2pack(terms.sc, terms.sc);
+          uint64_t ramp[LINEAR ? 16 : 1];
+          if (LINEAR) {
+#pragma unroll
+            for (int x = 0; x < 16; ++x) ramp[x] = f2pack(sl * (2 * x), sl * (2 * x + 1));
+          }
+          auto chunk_shift = [&](int ch) { return fmaf(sl, bias.off0 + static_cast<float>(32 * ch), bias.flat); };
           uint32_t r[W];
           uint32_t dead = 0;   // chunks that no row of the warp sees
           auto load = [&](int ch) {
@@ -577,17 +589,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dead |= 1u << ch;
                 continue;
               }
+              if constexpr (LINEAR) {   // (r keeps the raw scores for the second pass)
+                float c0 = -INFINITY, c1 = -INFINITY;
 #pragma unroll
-              for (int x = 0; x < W; x += 4) {
-                mx0 = fmax3(mx0, u2f(r[x]), u2f(r[x + 1]));
-                mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
+                for (int x = 0; x < W; x += 4) {
+                  float y0, y1, y2, y3;
+                  f2unpack(ffma2(pair_of(r, x), sc2, ramp[x / 2]), y0, y1);
+                  f2unpack(ffma2(pair_of(r, x + 2), sc2, ramp[x / 2 + 1]), y2, y3);
+                  c0 = fmax3(c0, y0, y1);
+                  c1 = fmax3(c1, y2, y3);
+                }
+                mx0 = fmaxf(mx0, fmaxf(c0, c1) + chunk_shift(ch));
+              } else {
+#pragma unroll
+                for (int x = 0; x < W; x += 4) {
+                  mx0 = fmax3(mx0, u2f(r[x]), u2f(r[x + 1]));
+                  mx1 = fmax3(mx1, u2f(r[x + 2]), u2f(r[x + 3]));
+                }
               }
               if ((!RAW || CUT) && !FEW) {   // one chunk stays in registers
 #pragma unroll
                 for (int x = 0; x < W; x += 32) tmem_st32(t_s + ch * W + x, *reinterpret_cast<uint32_t(*)[32]>(&r[x]));
               }
             }
-            const float m_cand = fmaf(fmaxf(mx0, mx1), scale, offset);
+            const float m_cand = LINEAR ? mx0 : fmaf(fmaxf(mx0, mx1), scale, offset);
             best = fmaxf(best, m_cand);
             // The reference: the first tile's maximum, raised (and O and l
             // rescaled) only by more than the threshold.  While a row has seen
@@ -606,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // Second pass: probabilities, stored as bf16 pairs over the scores
           // already read, and their fp32 sum.
-          const float neg = (m == -INFINITY ? 0.f : -m) + offset;
+          const float neg = (m == -INFINITY ? 0.f : -m) + (LINEAR ? 0.f : offset);
           const uint64_t negm = f2pack(neg, neg), scale2 = f2pack(scale, scale);
           float pm0 = 0.f, pm1 = 0.f;
 #pragma unroll 1
@@ -627,10 +652,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
               }
             }
+            const float shift = LINEAR ? neg + chunk_shift(ch) : 0.f;
+            const uint64_t shift2 = f2pack(shift, shift);
 #pragma unroll
             for (int x = 0; x < W / 2; ++x) {
               uint64_t y = pair_of(r, 2 * x);
-              if (!(F & kBounded)) y = ffma2(y, scale2, negm);
+              if (LINEAR) y = fadd2(ffma2(y, sc2, ramp[LINEAR ? x : 0]), shift2);
+              else if (!(F & kBounded)) y = ffma2(y, scale2, negm);
               float xl, xh;
               f2unpack(y, xl, xh);
               xl = ex2_approx(xl);
@@ -649,7 +677,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (F & kBounded) best = fmaxf(best, fmaxf(pm0, pm1));
         };
         if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) softmax(IntC<kCutTile>{});
-        else if ((F & 3) == kBias && a.slopes == nullptr && !bias.window) softmax(IntC<kFlatTile>{});
+        else if ((F & 3) == kBias && !bias.window && a.slopes == nullptr) softmax(IntC<kFlatTile>{});
+        else if ((F & 3) == kBias && !bias.window) softmax(IntC<kLinearTile>{});
         else softmax(IntC<kFullTile>{});
         if (FEW) {   // the other warps' columns are 0 in these lanes
           uint32_t pk[16];
