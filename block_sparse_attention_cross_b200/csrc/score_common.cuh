@@ -256,6 +256,7 @@ struct ScoreTerms {
   float sc;                  // scale log2e
   float capA, kcap, small;   // cap log2e; 2 log2e scale / cap; largest |s| for the polynomial
   float inv;                 // 1 / (cap log2e)
+  float shift;               // added to the capped score where there is no bias
   float c[5];                // capped score = s (c0 + c1 s^2 + ... + c4 s^8)
 };
 __device__ __forceinline__ ScoreTerms score_terms(const ScoreArgs& a) {
@@ -326,7 +327,7 @@ __device__ __forceinline__ void cap_polynomial(const ScoreTerms& t, uint32_t (&r
     if (FACTOR) {
       const uint64_t y = fmul2(s, q);
       f2unpack(ffma2(fmul2(y, y), ninv2, one), f[x], f[x + 1]);
-      set_pair(r, x, BIAS ? fadd2(y, shift2) : y);
+      set_pair(r, x, BIAS ? fadd2(y, shift2) : y);   // (the backward has no other shift)
     } else {
       set_pair(r, x, ffma2(s, q, shift2));
     }
@@ -354,7 +355,7 @@ __device__ __forceinline__ void score_columns(const ScoreArgs& a, const ScoreTer
   // of column 0 where the distance is linear over the tile.
   const bool slopes = (F & kBias) && a.slopes != nullptr, linear = slopes && (!BENT || b.side != 0);
   const float sl = b.side > 0 ? -b.slope : b.slope;   // -slope |off0 + DIR x| = sl (off0 + DIR x)
-  const float shift = F & kBias ? (b.window ? 0.f : b.flat) + (linear ? sl * b.off0 : 0.f) : 0.f;
+  const float shift = F & kBias ? (b.window ? 0.f : b.flat) + (linear ? sl * b.off0 : 0.f) : t.shift;
   if (F & kCap) {
     if (form == kAny || (form == kByScore && score_extent(r) <= t.small)) cap_polynomial<FACTOR, (F & kBias) != 0>(t, r, f, shift);
     else cap_mufu<FACTOR>(t, r, f, shift);

@@ -5,7 +5,8 @@
 // core alternates between the slots, so that one slot's softmax runs while the
 // other slot's products do.  Warps 0-3 and 4-7: softmax of slots 0 and 1;
 // warps 8 and 11: TMA producers, one K/V ring each; warp 9 issues every
-// tcgen05.mma; warp 10 idles.  TMEM: slot s owns columns [256 s, 256 s + 256):
+// tcgen05.mma; warp 10 fills the table's windows (score_common.cuh).  TMEM:
+// slot s owns columns [256 s, 256 s + 256):
 // scores at + 0 (the probabilities overwrite their first half as bf16 pairs,
 // the A operand of the second product), O at + 128.
 //
@@ -13,8 +14,9 @@
 //  - a tile walks the 128-key tiles of its rows' interval range, restricted to
 //    the calibrated mask's kept blocks where one is given, and only tiles
 //    that the interval of some row cuts pay for an element mask;
-//  - the scores pass through the cap, the distance bias and the table before
-//    the softmax, in registers;
+//  - the scores pass through the cap, the distance bias and the table in
+//    chunks of 32 columns, kept in TMEM between the pass that finds the maximum
+//    and the one that exponentiates; a cap without a bias needs no maximum;
 //  - tensors are 4-D maps with their own strides, so lengths need no padding
 //    and rows past a length read as zero;
 //  - the G query heads of a key head share one tile when their rows fit (few
@@ -183,9 +185,10 @@ constexpr int kFew = 8;
 // distance passes 0); and, without a cap, whole ones with one table value and
 // no slope, or with a slope and one table value.
 enum TileKind { kFullTile, kCutTile, kFlatTile, kLinearTile };
-// Largest cap in log2 units that goes without a maximum: probabilities
-// 2^score lie in 2^+-80, their sums over 2^24 keys and their products with V
-// (|v| < 2^20) inside fp32, and bf16 has fp32's exponents.
+// Largest cap in log2 units that goes without a maximum.  The reference is a
+// quarter of the cap: probabilities lie in 2^-100 ... 2^60, so that sums over
+// 2^24 keys stay inside fp32 for |v| < 2^43, rows whose scores are all at -cap
+// keep full precision down to |v| = 2^-26, and bf16 has fp32's exponents.
 constexpr float kBoundedCap = 80.f;
 
 template <int D, int F>
@@ -424,7 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t t_s = tmem + (static_cast<uint32_t>(w4 * 32) << 16) + slot * 256;
     const uint32_t t_o = t_s + 128;
     // Scores are in log2 units.
-    const ScoreTerms terms = score_terms(a);
+    ScoreTerms terms = score_terms(a);
+    if (F & kBounded) terms.shift = -0.25f * terms.capA;
     uint32_t gb = 0, nw = 0;   // key tiles and windows consumed
     int tiles = 0;
     bool ok = true, corrupt = false;
@@ -476,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         far_lo = __bfloat162float(tab[score_bucket(a, -a.R, &corrupt)]) * kLog2e;
         far_hi = __bfloat162float(tab[score_bucket(a, a.R, &corrupt)]) * kLog2e;
       }
-      float m = F & kBounded ? 0.f : -INFINITY, l = 0.f;
+      float m = F & kBounded ? 0.25f * terms.capA : -INFINITY, l = 0.f;
       float best = F & kBounded ? 0.f : -INFINITY;   // kBounded: largest probability; else largest score
       bool row_bad = false;
       bool scanned = false;      // the step before this one listed bad keys
@@ -677,8 +681,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (F & kBounded) best = fmaxf(best, fmaxf(pm0, pm1));
         };
         if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) softmax(IntC<kCutTile>{});
-        else if ((F & 3) == kBias && !bias.window && a.slopes == nullptr) softmax(IntC<kFlatTile>{});
-        else if ((F & 3) == kBias && !bias.window) softmax(IntC<kLinearTile>{});
+        else if (!FEW && (F & 3) == kBias && !bias.window && a.slopes == nullptr) softmax(IntC<kFlatTile>{});
+        else if (!FEW && (F & 3) == kBias && !bias.window) softmax(IntC<kLinearTile>{});
         else softmax(IntC<kFullTile>{});
         if (FEW) {   // the other warps' columns are 0 in these lanes
           uint32_t pk[16];

@@ -236,6 +236,17 @@ def test_caps_of_every_size(dtype, cap, scale):
     Case(H=1, Nq=150, d=64, dtype=dtype, cap=cap, scale=scale, gain=1e-2 if cap > 1e4 and scale > 1 else 1.0).check()
 
 
+# values far from 1 on either side, every score at the cap's negative end for some rows
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("size", [1e9, 1e-6])
+def test_sizes_of_values_under_a_cap(dtype, size):
+    c = Case(H=2, Nq=200, d=64, dtype=dtype, cap=55.0, scale=8.0, gain=4.0)
+    c.v = (c.v.float() * size).to(dtype)
+    c.k[0, 0] = c.k[0, 0, :1]
+    c.q[0, 0, 50:120] = -8 * c.k[0, 0, 0]
+    c.check(train=False)
+
+
 def test_integers_of_any_width_and_place():
     want = cba.attn_spans(2, 40, 50, causal=True, kv_len=[50, 7], q_start=[10, 0], prefix=[3, 60])
     got = cba.attn_spans(2, 40, 50, causal=True, kv_len=torch.tensor([1 << 40, 7], device="cuda"),
