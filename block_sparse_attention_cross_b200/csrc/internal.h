@@ -123,7 +123,7 @@ int launch_score_fwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_score_bwd_simt(const ScoreArgs& a, int d, cudaStream_t s);
 // score_fwd.cu (bf16, tcgen05)
 bool score_packs(int G, int Nq, bool mask, bool table);
-int score_splits(int B, int heads, int nq_tiles, bool few, int nkb);
+int score_splits(int B, int heads, int nq_tiles, int nkb);
 int score_kv_parts(int B, int Hkv, int G, int nqb, int nkb);   // score_bwd.cu
 int launch_score_bwd_tc(const ScoreArgs& a, int d, cudaStream_t s);
 int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s);

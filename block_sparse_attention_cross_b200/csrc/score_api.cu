@@ -127,7 +127,7 @@ size_t fwd_layout(ScoreArgs& a, int d, void* ws) {
 void fwd_plan(ScoreArgs& a, bool packed) {
   a.packed = packed;
   a.few = packed && a.G * a.Nq <= 32;
-  a.splits = score_splits(a.B, packed ? a.Hkv : a.H, packed ? 1 : a.nqb, a.few != 0, a.nkb);
+  a.splits = score_splits(a.B, packed ? a.Hkv : a.H, packed ? 1 : a.nqb, a.nkb);
   a.parts = a.few ? 4 * a.splits : a.splits;
 }
 

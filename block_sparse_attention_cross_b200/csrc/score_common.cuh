@@ -173,7 +173,8 @@ __device__ __forceinline__ void keep_bits(uint32_t (&r)[32], uint32_t bits, floa
 
 // The boxes of row `row` of a tile of 128 rows: each zeroed where it holds a
 // NaN or an infinity; whether one did.  Out of line: only tiles that the mask
-// cuts need it.
+// cuts need it.  Called with no TMEM load or store in flight: their registers
+// are not safe across a call.
 template <int BOXES>
 __device__ __noinline__ bool clean_row(uint8_t* tile, int row) {
   bool bad = false;

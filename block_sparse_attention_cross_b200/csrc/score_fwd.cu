@@ -35,8 +35,9 @@
 // 1660 of products.  24 heads of 8192 tokens, d = 128: 0.91 ms plain (907
 // TFLOP/s), 1.14 capped, 1.13 with slopes, 1.04 with a table.  (Two warpgroups
 // a slot, half of the columns each: capped 1.10, but plain 0.96, a table 1.30
-// ms.)  Few queries: HBM; 32 sequences of up to 8191 keys read 670 MB in 0.16
-// ms (4.2 TB/s, 65% of the measured copy).
+// ms.)  Few queries: HBM; 4 tokens of 24 heads read 930 MB of K and V in 0.15
+// ms (6.2 TB/s, 96% of the measured copy), 32 sequences of different lengths
+// 670 MB in 0.16 ms (the longest sequences last).
 #include <algorithm>
 #include <atomic>
 
@@ -247,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0;
     int qf = 0;
     bool ok = true;
-    const uint64_t pol = l2_policy_evict_last(), pol_q = l2_policy_evict_first();
+    // (with few queries K and V are read once)
+    const uint64_t pol_q = l2_policy_evict_first(), pol = FEW ? pol_q : l2_policy_evict_last();
     uint8_t* ring = smem + L::OFF_RING + s * R * L::TBYTES;
     const int copies = FEW ? 4 : 1;
     const uint32_t q_bytes = a.packed ? static_cast<uint32_t>(copies * a.G * a.Nq * D * 2) : L::TBYTES;
@@ -822,17 +824,16 @@ bool score_packs(int G, int Nq, bool mask, bool table) {
   return static_cast<long long>(G) * Nq <= TILE && !mask && (!table || G <= kMaxPackedTable);
 }
 
-// Splits of the key axis, for 296 slots (two on each of 148 SMs) of one unit
-// (query tile and split) at a time.  Units of equal length fill whole rounds
-// of the slots when there are floor(296 rounds / tiles) splits of each tile.
-// Tiles of few rows (serving) write little per split and their sequences
-// differ in length, so they take four rounds, at least two key tiles a
-// split; full tiles write 512 bytes of partial sums per row and split, so they
-// are split into one round, and only when they leave half of the slots idle.
-int score_splits(int B, int heads, int nq_tiles, bool few, int nkb) {
+// Splits of the key axis, at least two key tiles each, for 296 slots (two on
+// each of 148 SMs) of one unit (query tile and split) at a time: as many as
+// still fit one round of the slots.  A unit costs about as much as a key tile
+// (its last product, its partial results), so finer splits, which would even
+// out sequences of different lengths, lose more than they win: 4 tokens, 24
+// heads, 75 600 keys 150 us in one round, 165 in two, 180 in four; 32
+// sequences of 2500 ... 8191 keys 162, 174, 160; 8 of 4800 ... 16 000 76, 70, 82.
+int score_splits(int B, int heads, int nq_tiles, int nkb) {
   const long long tiles = static_cast<long long>(B) * heads * nq_tiles;
-  const long long want = (few ? 4 : 1) * 296 / tiles;
-  return static_cast<int>(std::max<long long>(1, std::min<long long>(want, nkb / 2)));
+  return static_cast<int>(std::max<long long>(1, std::min<long long>(296 / tiles, nkb / 2)));
 }
 
 int launch_score_fwd_tc(const ScoreArgs& a, int d, cudaStream_t s) {
