@@ -623,7 +623,7 @@ template <int RK, int RV>
 struct DqCtrl {
   uint64_t q_full, k_full[RK], k_empty[RK], v_full[RV], v_empty[RV];
   uint64_t a_full[2], a_free[2], mid;   // first sweep
-  uint64_t s_full[2], dp_full, dp_free, ds_full, o_full, drain;
+  uint64_t s_full[2], dp_full, dp_free, ds_full[2], o_full, drain;
   uint64_t win_full[2], win_empty[2];
   WindowInfo win_info[2];
   uint32_t tmem_base;
@@ -637,7 +637,10 @@ struct DqCtrl {
 // dQ at 384.  Issue order: S(0), dP(0), S(1); then per tile t, once dP(t) is
 // read, dP(t + 1), and once dS(t) is stored, dQ(t) and S(t + 2): the scores are
 // a tile ahead and dP(t + 1) is formed during the second half of tile t's
-// arithmetic.
+// arithmetic.  A warp may therefore store dS(t + 1) before a slower one has
+// stored dS(t) (the table's gradient takes longer near the diagonal): tiles
+// alternate between two ds_full barriers.  It gets no further ahead, since
+// S(t + 2) waits for dS(t).
 // Adds the warp's sum of v to *acc, in a fixed order.
 __device__ __forceinline__ void add_to_bucket(float* acc, float v) {
 #pragma unroll
@@ -648,7 +651,7 @@ __device__ __forceinline__ void add_to_bucket(float* acc, float v) {
 
 // dZ of 32 columns whose offsets meet boundaries k ... k1 - 1 of a window:
 // column x is entry `entry` + x.  Per segment the row's sum, added up over the
-// warp.  (Out of line, as the next one: few tiles near the diagonal need them.)
+// warp.
 __device__ __forceinline__ void sum_by_cuts(const uint32_t (&g)[32], const WindowInfo& info, int k, int k1, int entry,
                                          float* acc) {
   float before = 0.f;
@@ -734,13 +737,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&c->a_full[e], 1);
       mbar_init(&c->a_free[e], 256);
       mbar_init(&c->s_full[e], 1);
+      mbar_init(&c->ds_full[e], 256);
       mbar_init(&c->win_full[e], 32);
       mbar_init(&c->win_empty[e], 256);
     }
     mbar_init(&c->mid, 256);
     mbar_init(&c->dp_full, 1);
     mbar_init(&c->dp_free, 256);
-    mbar_init(&c->ds_full, 256);
     mbar_init(&c->o_full, 1);
     mbar_init(&c->drain, 1);
     c->abort = 0;
@@ -869,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t t = 0; t < n; ++t) {
         if (!wait(&c->dp_free, t & 1)) break;
         if (t + 1 < n && !grads(t + 1)) break;
-        if (!wait(&c->ds_full, t & 1)) break;
+        if (!wait(&c->ds_full[t & 1], (t >> 1) & 1)) break;
         mma_from_tmem(tQ, tmem + (t & 1) * 128, sK(n + t), IDESC_O, t > 0 ? 1u : 0u);
         mma_commit_w(&c->k_empty[(n + t) % RK]);
         if (t + 1 == n) mma_commit_w(&c->o_full);
@@ -978,13 +981,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           bucket = info.bucket[k];
         }
         if (info.cuts > kMaxCuts || k != k1) {
-          // (a copy: an array whose address is taken lives in local memory, and
-          // the TMEM load would be stored there before it has arrived)
-          uint32_t copy[32];
-#pragma unroll
-          for (int x = 0; x < 32; ++x) copy[x] = g[x];
-          if (info.cuts <= kMaxCuts) sum_by_cuts(copy, info, k, k1, TILE - 1 - row + c0, hist + warp * 256);
-          else sum_by_diagonals(copy, smem + L::OFF_BWIN + (wt & 1) * 256 + first, hist + warp * 256);
+          if (info.cuts <= kMaxCuts) sum_by_cuts(g, info, k, k1, TILE - 1 - row + c0, hist + warp * 256);
+          else sum_by_diagonals(g, smem + L::OFF_BWIN + (wt & 1) * 256 + first, hist + warp * 256);
           return;
         }
       }
@@ -1153,7 +1151,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&c->ds_full);
+        mbar_arrive(&c->ds_full[t & 1]);
       };
       if (edge || ((F & kBias) && a.slopes != nullptr && bias.side == 0)) tile(IntC<1>{});
       else tile(IntC<0>{});

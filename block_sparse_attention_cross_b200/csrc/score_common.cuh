@@ -360,6 +360,7 @@ __device__ __forceinline__ void score_columns(const ScoreArgs& a, const ScoreTer
   if (F & kCap) {
     if (form == kAny || (form == kByScore && score_extent(r) <= t.small)) cap_polynomial<FACTOR, (F & kBias) != 0>(t, r, f, shift);
     else cap_mufu<FACTOR>(t, r, f, shift);
+    __syncwarp();   // rows of a warp may take either form, and the tensor-memory accesses that follow need all lanes
   } else {
     const uint64_t sc = f2pack(t.sc, t.sc), shift2 = f2pack(shift, shift);
 #pragma unroll

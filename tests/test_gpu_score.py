@@ -179,6 +179,24 @@ def test_deterministic_and_graph_replay():
         assert torch.equal(o2, first["o"][:1])
 
 
+@pytest.mark.parametrize("kw", [dict(cap=50.0, prefix=[1000]), dict(prefix=[1000]),
+                                dict(cap=50.0, docs=[[0, 700, 1500, 2046]], prefix=[[650, 500, 546]])])
+def test_repeated_backward_is_bit_equal(kw):
+    # Rows before the prefix's end see keys after them (one bucket, summed fast) and near the diagonal many buckets
+    # (summed slowly): the warps of a tile run apart, and no tile may be used before the slowest has stored its part.
+    N = 2046
+    c = Case(H=16, Hkv=4, Nq=N, d=128, buckets=64, distance=8192, bidirectional=False, causal=True, **kw)
+    skw, sp = c.score_kw(), c.spans()
+    q, k, v, do = (c.gpu(x) for x in (c.q, c.k, c.v, c.do))
+    o, lse = cba.score_attn_fwd(q, k, v, sp, return_lse=True, **skw)
+    first = cba.score_attn_bwd(do, q, k, v, o, lse, sp, **skw)
+    assert all(torch.isfinite(x).all() for x in first)
+    for _ in range(20):
+        again = cba.score_attn_bwd(do, q, k, v, o, lse, sp, **skw)
+        for name, x, y in zip(("dq", "dk", "dv", "dtable"), first, again):
+            assert torch.equal(x, y), name
+
+
 def test_caller_buffers_and_refusals():
     c = Case(B=1, H=2, Nq=33, d=64, buckets=4, distance=3)
     q, k, v = (c.gpu(x) for x in (c.q, c.k, c.v))
