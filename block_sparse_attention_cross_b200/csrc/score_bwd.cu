@@ -456,8 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             at.off0 -= static_cast<float>(32 * c32);
             at.wr -= 32 * c32;
             score_columns<F, -1, true, CUT>(a, terms, *reinterpret_cast<uint32_t(*)[32]>(&r[c32 * 32]),
-                                            *reinterpret_cast<float(*)[32]>(&pf[c32 * 32]), at,
-                                            CUT && edge ? kExact : kByScore);
+                                            *reinterpret_cast<float(*)[32]>(&pf[c32 * 32]), at);
             if (c32 == 1 && near) mbar_arrive(&c->win_empty[nw & 1]);
           }
           float pv[32];
@@ -1032,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             at.off0 += static_cast<float>(32 * ch);
             at.wr += 32 * ch;
             float none[32];
-            score_columns<F & 3, 1, false, CUT>(a, terms, r, none, at, CUT && ~bits != 0 ? kExact : kByScore);
+            score_columns<F & 3, 1, false, CUT>(a, terms, r, none, at);
           }
           if (CUT) {
             keep_bits(r, bits, -INFINITY);
@@ -1120,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ScoreBias at = bias;
             at.off0 += static_cast<float>(32 * ch);
             at.wr += 32 * ch;
-            score_columns<F & 3, 1, (F & kCap) != 0, CUT>(a, terms, r, f, at, CUT && ~bits != 0 ? kExact : kByScore);
+            score_columns<F & 3, 1, (F & kCap) != 0, CUT>(a, terms, r, f, at);
           }
           // dZ = P (dP - D) in place of dP
 #pragma unroll

@@ -246,37 +246,42 @@ __device__ __forceinline__ void fill_window(const ScoreArgs& a, int h0, int head
 }
 
 // ---- the score function on the columns of a thread's row ---------------------
-// In log2 units.  cap tanh(s scale / cap): where every |s scale / cap| of the
-// thread's columns is at most 0.6, an odd polynomial on the FMA pipe;
-// elsewhere cap - 2 cap / (1 + e^(2x)), two MUFU operations a score, right at
-// both ends.  Both stay within 3e-7 of the cap.  The polynomial leaves the
-// MUFU, which bounds the softmax, to the exponentials.  A row chooses by its
-// own scores, and where the mask cuts it (kExact) always takes the second
-// form, so no other row and no masked place changes a bit of it.
+// In log2 units.  cap tanh(x), x = s scale / cap: where |x| is at most 0.45, s
+// times a polynomial in x^2 on the FMA pipe, whose error is relative to the
+// score; beyond, cap - 2 cap / (1 + e^(2x)), two MUFU operations a score, right
+// at both ends, off by up to 3e-7 of the cap, which is 7e-7 of a score of that
+// size.  (That form alone is not enough: of scores far below the cap it leaves
+// the cap's last bits, 12% of a score at a millionth of it.)  The polynomial
+// leaves the MUFU, which bounds the softmax, to the exponentials.  Every score
+// chooses by itself, so no other row and no masked place changes a bit of it;
+// a row without large ones skips the second form.
 struct ScoreTerms {
   float sc;                  // scale log2e
   float capA, kcap, small;   // cap log2e; 2 log2e scale / cap; largest |s| for the polynomial
-  float inv;                 // 1 / (cap log2e)
+  float k, ninv2;            // scale / cap; -1 / (cap log2e)^2
   float shift;               // added to the capped score where there is no bias
-  float c[5];                // capped score = s (c0 + c1 s^2 + ... + c4 s^8)
+  float c[4];                // capped score = s (c0 + c1 x^2 + c2 x^4 + c3 x^6), x = k s
 };
 __device__ __forceinline__ ScoreTerms score_terms(const ScoreArgs& a) {
   ScoreTerms t = {};
   t.sc = a.scale * kLog2e;
   if (a.cap > 0.f) {
-    const float k = a.scale / a.cap, k2 = k * k;
+    t.k = a.scale / a.cap;
     t.capA = a.cap * kLog2e;
-    t.kcap = 2.f * kLog2e * k;
-    // (the coefficients hold powers of k up to the eighth: only where those stay far inside fp32)
-    t.small = k > 1e-4f && k < 1e3f ? 0.6f / k : -1.f;
-    t.inv = 1.f / t.capA;
-    // tanh(x) / x as a polynomial in x^2, interpolated at the five Chebyshev
-    // nodes of [0, 0.36] (relative error at most 8e-8)
-    t.c[0] = 0.999999926f * t.sc;
-    t.c[1] = -0.333323020f * t.sc * k2;
-    t.c[2] = 0.133100644f * t.sc * k2 * k2;
-    t.c[3] = -0.052096653f * t.sc * k2 * k2 * k2;
-    t.c[4] = 0.015468751f * t.sc * k2 * k2 * k2 * k2;
+    t.kcap = 2.f * kLog2e * t.k;
+    // (1 / cap^2 must stay finite; under smaller caps the second form's error,
+    // relative to the cap, is nothing to the scores)
+    t.small = a.cap > 1e-18f ? 0.45f / t.k : -1.f;
+    t.ninv2 = -(1.f / t.capA) * (1.f / t.capA);
+    // tanh(x) / x as a polynomial in x^2, interpolated at the four Chebyshev
+    // nodes of [0, 0.2025] (relative error at most 2.6e-7).  The powers of x
+    // are formed from x itself: coefficients with powers of scale / cap would
+    // underflow under large caps.  (Five terms, right to 8e-8 up to 0.6: 24
+    // heads of 8192 tokens, d = 128, 1217 us instead of 1135.)
+    t.c[0] = 0.999999762f * t.sc;
+    t.c[1] = -0.333294511f * t.sc;
+    t.c[2] = 0.132361695f * t.sc;
+    t.c[3] = -0.0460216627f * t.sc;
   }
   return t;
 }
@@ -315,51 +320,57 @@ __device__ __forceinline__ float score_extent(const uint32_t (&r)[N]) {
   return fmaxf(big0, big1);
 }
 
-// The capped score by the polynomial, plus `shift`; f: the cap's derivative.
+// The capped scores s of two columns by the polynomial, plus `shift`; f: the cap's derivative.
+template <bool FACTOR, bool BIAS>
+__device__ __forceinline__ uint64_t cap_pair(const ScoreTerms& t, uint64_t s, uint64_t shift2, float& f0, float& f1) {
+  const uint64_t x = fmul2(s, f2pack(t.k, t.k)), v = fmul2(x, x);
+  uint64_t q = f2pack(t.c[3], t.c[3]);
+#pragma unroll
+  for (int i = 2; i >= 0; --i) q = ffma2(q, v, f2pack(t.c[i], t.c[i]));
+  if (!FACTOR) return ffma2(s, q, shift2);
+  const uint64_t y = fmul2(s, q);
+  f2unpack(ffma2(fmul2(y, f2pack(t.ninv2, t.ninv2)), y, f2pack(1.f, 1.f)), f0, f1);
+  return BIAS ? fadd2(y, shift2) : y;   // (the backward has no other shift)
+}
 template <bool FACTOR, bool BIAS, int N>
 __device__ __forceinline__ void cap_polynomial(const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N], float shift) {
-  const uint64_t c0 = f2pack(t.c[0], t.c[0]), c1 = f2pack(t.c[1], t.c[1]), c2 = f2pack(t.c[2], t.c[2]),
-                 c3 = f2pack(t.c[3], t.c[3]), c4 = f2pack(t.c[4], t.c[4]), shift2 = f2pack(shift, shift);
-  const uint64_t ninv2 = f2pack(-t.inv * t.inv, -t.inv * t.inv), one = f2pack(1.f, 1.f);
+  const uint64_t shift2 = f2pack(shift, shift);
+#pragma unroll
+  for (int x = 0; x < N; x += 2) set_pair(r, x, cap_pair<FACTOR, BIAS>(t, pair_of(r, x), shift2, f[x], f[x + 1]));
+}
+// Either form, score by score.
+template <bool FACTOR, bool BIAS, int N>
+__device__ __forceinline__ void cap_mixed(const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N], float shift) {
+  const uint64_t shift2 = f2pack(shift, shift);
 #pragma unroll
   for (int x = 0; x < N; x += 2) {
-    const uint64_t s = pair_of(r, x), v = fmul2(s, s);
-    const uint64_t q = ffma2(ffma2(ffma2(ffma2(c4, v, c3), v, c2), v, c1), v, c0);
-    if (FACTOR) {
-      const uint64_t y = fmul2(s, q);
-      f2unpack(ffma2(fmul2(y, y), ninv2, one), f[x], f[x + 1]);
-      set_pair(r, x, BIAS ? fadd2(y, shift2) : y);   // (the backward has no other shift)
-    } else {
-      set_pair(r, x, ffma2(s, q, shift2));
-    }
-  }
-}
-template <bool FACTOR, int N>
-__device__ __forceinline__ void cap_mufu(const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N], float shift) {
+    const float s[2] = {u2f(r[x]), u2f(r[x + 1])};
+    set_pair(r, x, cap_pair<FACTOR, BIAS>(t, f2pack(s[0], s[1]), shift2, f[x], f[x + 1]));
 #pragma unroll
-  for (int x = 0; x < N; ++x) {
-    const float rc = rcp_approx(1.f + ex2_approx(u2f(r[x]) * t.kcap));
-    if (FACTOR) f[x] = 4.f * (rc - rc * rc);
-    r[x] = f2u(fmaf(-2.f * t.capA, rc, t.capA) + shift);
+    for (int e = 0; e < 2; ++e) {   // (no branches: the two forms of different scores run beside each other)
+      const bool large = fabsf(s[e]) > t.small;
+      const float rc = rcp_approx(1.f + ex2_approx(s[e] * t.kcap));
+      if (FACTOR) f[x + e] = large ? 4.f * (rc - rc * rc) : f[x + e];
+      r[x + e] = large ? f2u(fmaf(-2.f * t.capA, rc, t.capA) + shift) : r[x + e];
+    }
   }
 }
 
 // The score function.  DIR = 1: the columns are keys; DIR = -1: queries.
-// BENT: the distance may pass 0 inside the tile.  form: the cap's, by the row's
-// scores (kByScore), the second (kExact) or the polynomial (kAny: rows whose
-// result nobody reads, which must not drag their warp through both).
-enum CapForm { kByScore, kExact, kAny };
+// BENT: the distance may pass 0 inside the tile.  live = false: a row whose
+// result nobody reads, which must not drag its warp through the cap's second
+// form.
 template <int F, int DIR, bool FACTOR, bool BENT, int N>
 __device__ __forceinline__ void score_columns(const ScoreArgs& a, const ScoreTerms& t, uint32_t (&r)[N], float (&f)[N],
-                                              const ScoreBias& b, int form) {
+                                              const ScoreBias& b, bool live = true) {
   // The constant part of the biases: the flat table value, and the distance
   // of column 0 where the distance is linear over the tile.
   const bool slopes = (F & kBias) && a.slopes != nullptr, linear = slopes && (!BENT || b.side != 0);
   const float sl = b.side > 0 ? -b.slope : b.slope;   // -slope |off0 + DIR x| = sl (off0 + DIR x)
   const float shift = F & kBias ? (b.window ? 0.f : b.flat) + (linear ? sl * b.off0 : 0.f) : t.shift;
   if (F & kCap) {
-    if (form == kAny || (form == kByScore && score_extent(r) <= t.small)) cap_polynomial<FACTOR, (F & kBias) != 0>(t, r, f, shift);
-    else cap_mufu<FACTOR>(t, r, f, shift);
+    if (live && score_extent(r) > t.small) cap_mixed<FACTOR, (F & kBias) != 0>(t, r, f, shift);
+    else cap_polynomial<FACTOR, (F & kBias) != 0>(t, r, f, shift);
     __syncwarp();   // rows of a warp may take either form, and the tensor-memory accesses that follow need all lanes
   } else {
     const uint64_t sc = f2pack(t.sc, t.sc), shift2 = f2pack(shift, shift);

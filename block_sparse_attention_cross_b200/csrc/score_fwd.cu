@@ -579,8 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               at.off0 += static_cast<float>(W * ch);
               at.wr += W * ch;
               float none[W];
-              score_columns<F & 3, 1, false, CUT>(a, terms, r, none, at,
-                                                 !live ? kAny : CUT && ~bits != 0 ? kExact : kByScore);
+              score_columns<F & 3, 1, false, CUT>(a, terms, r, none, at, live);
             }
             if constexpr (CUT) keep_bits(r, bits, -INFINITY);
             return true;

@@ -51,3 +51,40 @@ def test_calibrated_mask(dtype, kw):
     m = (np.random.default_rng(7).random((2, 4, 4)) < 0.5).astype(np.uint8)
     m[1, 2] = 0
     Narrow(H=2, Nq=450, d=128, dtype=dtype, mask=torch.from_numpy(m), **kw).verify()
+
+
+# caps far above the scores: cap tanh(s / cap) is the score itself there
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rules", [dict(), dict(causal=True)])       # whole tiles; tiles that the mask cuts
+@pytest.mark.parametrize("cap", [1e3, 1e4, 1e5, 1e6, 1e9, 1e20, 8e37])
+def test_caps_above_the_scores(dtype, rules, cap):
+    kw = dict(H=2, Nq=256, d=64, dtype=dtype, gain=3.0, **rules)
+    c = Narrow(cap=cap, **kw)
+    got, ref = c.verify()
+    # The same call without a cap, which moves a score of at most 16 by s^3 / 3 cap^2 < 2e-7.  fp32: four roundings of the
+    # score, 4 x 16 x 2^-24 in P, twice through the normaliser and twice in P (dP - D): 2^-16.  bf16: a rounding of P, dS or
+    # the result may fall to the other side.
+    if cap >= 1e5:
+        want = Narrow(**kw).run(True)
+        for n in ("o", "dq", "dk", "dv"):
+            x, y = got[n], want[n].double().cpu().numpy()
+            assert np.linalg.norm(x - y) <= (2.0 ** -8 if dtype == BF else 2.0 ** -16) * np.linalg.norm(y), n
+
+
+# a large cap with a few scores near it, of either sign, among small ones: each score is capped by itself
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bias", [dict(), dict(slopes=True, buckets=8, distance=30)])
+@pytest.mark.parametrize("cap,rules", [(1e4, dict()), (1e5, dict()), (1e5, dict(causal=True))])
+def test_large_and_small_scores_under_one_cap(dtype, bias, cap, rules):
+    c = Narrow(H=2, Nq=256, d=64, dtype=dtype, cap=cap, **bias, **rules)
+    c.k[:, :, ::37] = 0                               # columns with a score of 0 for every row,
+    c.k[:, :, 1::37] *= 0
+    c.k[:, :, 1::37, 0] = -cap * 8                    # and of about -cap q_0: far below the others or far above
+    c.q[:, :, :, 0] = c.q[:, :, :, 0].abs() + 0.25
+    c.verify()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("cap", [1e-30, 1e-5, 0.3, 60.0])
+def test_caps_below_the_scores(dtype, cap):
+    Narrow(H=2, Nq=200, d=64, dtype=dtype, cap=cap, scale=3.0 if cap > 1 else 0.125).verify()
