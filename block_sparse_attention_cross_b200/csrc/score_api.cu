@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kMaxBuckets = 256;
 constexpr int kMaxDistance = 1 << 20;
-constexpr long long kMaxLen = 1ll << 24;   // offsets stay exact in fp32
+constexpr long long kMaxLen = 1ll << 24;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

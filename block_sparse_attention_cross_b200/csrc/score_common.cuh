@@ -21,6 +21,15 @@ __device__ __forceinline__ int2 score_row(const ScoreArgs& a, int b, int i) {
   return r.x < r.y ? r : make_int2(0, 0);
 }
 
+// Whether the row at position p sees a key farther away than fp32 counts.
+// Positions go up to 2^30, and with rounded distances neighbouring keys would
+// get the same one, or jump by many: with a slope such a row becomes NaN
+// (through a NaN slope) and is reported.
+constexpr int kMaxSlopeDistance = 1 << 24;
+__device__ __forceinline__ bool score_far(int2 vis, int p) {
+  return vis.x < vis.y && max(abs(vis.x - p), abs(vis.y - 1 - p)) > kMaxSlopeDistance;
+}
+
 // Range of a query tile, clamped to the keys: x, y as score_row for the union
 // of its rows; keys inside [z, w) are seen by every row.
 __device__ __forceinline__ int4 score_tile(const ScoreArgs& a, int b, int qb) {

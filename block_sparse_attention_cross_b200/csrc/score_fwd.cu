@@ -474,7 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p0 = a.q_start[w.b] + (a.packed ? 0 : w.qb * TILE);   // positions of the tile's rows: p0 ... p1
       const int p1 = p0 + (a.packed ? a.Nq : TILE) - 1;
       const int p = a.q_start[w.b] + i;
-      const float slope = a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
+      float slope = a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
+      if ((F & kBias) && slope != 0.f && score_far(vis, p)) {
+        slope = NAN;
+        report_status(a.status, CALIBATT_E_UNSUPPORTED);
+      }
       const __nv_bfloat16* tab =
           reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
       float far_lo = 0.f, far_hi = 0.f;

@@ -228,7 +228,8 @@ def score_attn_fwd(q, k, v, spans: AttnSpans, *, scale=None, cap=0.0, slopes=Non
     contiguous and 16-byte aligned rows.  ``spans``: the keys every row sees
     (:func:`attn_spans`).  Scores: scale q.k (scale 1/sqrt(d) when None),
     capped to cap tanh(s / cap) when ``cap`` > 0, minus ``slopes``[h] |j - p|
-    ([H] float32), plus ``table``[h, buckets[j - p]] ([H, n_buckets] of q's
+    ([H] float32; rows that see keys farther away than 2^24 become NaN and are
+    reported to ``status``), plus ``table``[h, buckets[j - p]] ([H, n_buckets] of q's
     type; ``buckets`` int32 [2 max_distance + 1], e.g. from
     :func:`relative_buckets`).  ``mask``: uint8 [n_maps, nqb, nkb] kept 128 x
     128 blocks (as :func:`calibrate` returns), head h uses map ``map_offset``

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import block_sparse_attention_cross_b200 as cba
 from tests._score_check import Narrow
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +89,29 @@ def test_large_and_small_scores_under_one_cap(dtype, bias, cap, rules):
 @pytest.mark.parametrize("cap", [1e-30, 1e-5, 0.3, 60.0])
 def test_caps_below_the_scores(dtype, cap):
     Narrow(H=2, Nq=200, d=64, dtype=dtype, cap=cap, scale=3.0 if cap > 1 else 0.125).verify()
+
+
+# positions far behind the keys: with a slope rows farther from a visible key than fp32 counts (2^24) are refused
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Nq,Nk", [(150, 200), (2, 700)])            # whole tiles, few queries
+def test_far_positions_with_slopes(dtype, Nq, Nk):
+    lim = 1 << 24
+    starts = [1 << 26, lim - Nq + 1, -lim + Nk - 1, 7, 1 << 28]      # beyond, the farthest (both ways), near, beyond
+    kw = dict(B=5, H=2, Nq=Nq, Nk=Nk, d=64, dtype=dtype, q_start=starts, kv_len=[Nk, Nk, Nk, Nk, 0], q_len=[Nq] * 5)
+    c = Narrow(slopes=True, **kw)
+    c.slopes = torch.tensor([2.0 ** -18, 0.0])
+    q, k, v, do = (c.gpu(x) for x in (c.q, c.k, c.v, c.do))
+    st, sp, skw = torch.zeros(1, dtype=torch.int32, device="cuda"), c.spans(), c.score_kw()
+    o, lse = cba.score_attn_fwd(q, k, v, sp, return_lse=True, status=st, **skw)
+    grads = cba.score_attn_bwd(do, q, k, v, o, lse, sp, **skw)
+    assert st.item() == -2                                           # unsupported
+    assert o[0, 0].isnan().all() and lse[0, 0].isnan().all() and grads[0][0, 0].isnan().all()
+    assert grads[1][0, 0].isnan().all() and grads[2][0, 0].isnan().all()
+    # a head without a slope, the other batch entries and rows that see nothing are as ever
+    ref = c.reference(True)
+    got = {n: x.double().cpu().numpy() for n, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *grads))}
+    for n in got:
+        got[n][0, 0] = ref[n][0, 0]
+    assert c.faults(got, ref) == []
+    # learned buckets clip their offsets: no limit
+    Narrow(buckets=8, distance=30, **kw).verify()
