@@ -138,7 +138,7 @@ __device__ __forceinline__ void fill_window(const ScoreArgs& a, int h, int o0, W
   if (x < 2 * BT - 1) {
     const int n = score_bucket(a, o0 + x, bad);
     w->bucket[x] = n;
-    w->value[x] = reinterpret_cast<const float*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n];
+    w->value[x] = table_entry(reinterpret_cast<const float*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n]);
   }
 }
 

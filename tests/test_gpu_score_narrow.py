@@ -115,3 +115,25 @@ def test_far_positions_with_slopes(dtype, Nq, Nk):
     assert c.faults(got, ref) == []
     # learned buckets clip their offsets: no limit
     Narrow(buckets=8, distance=30, **kw).verify()
+
+
+# a bucket with the type's lowest value, or -inf, hides its keys; a row that sees nothing else is empty
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kw", [dict(), dict(slopes=True, cap=3.0)])
+@pytest.mark.parametrize("low", ["lowest", "-inf"])
+@pytest.mark.parametrize("Nq,Nk", [(300, 310), (3, 500)])
+def test_lowest_table_values_hide_keys(dtype, kw, low, Nq, Nk):
+    c = Narrow(B=2, H=2, Nq=Nq, Nk=Nk, d=64, dtype=dtype, buckets=8, distance=60, bidirectional=False, causal=True,
+               q_start=[-2, Nk - Nq], **kw)
+    R = len(c.buckets) // 2
+    c.buckets[R + 1:] = 7                       # keys after the query: hidden by the table instead of by the rule
+    c.buckets[:R + 1] = c.buckets[:R + 1].clamp(max=6)
+    c.table[:, 7] = torch.finfo(dtype).min if low == "lowest" else float("-inf")
+    q, k, v, do = (c.gpu(x) for x in (c.q, c.k, c.v, c.do))
+    sp, skw = cba.attn_spans(2, Nq, Nk, q_start=[-2, Nk - Nq]), c.score_kw()
+    o, lse = cba.score_attn_fwd(q, k, v, sp, return_lse=True, **skw)
+    grads = cba.score_attn_bwd(do, q, k, v, o, lse, sp, **skw)
+    c.table[:, 7] = 0                           # (no pair of the reference has bucket 7)
+    ref = c.reference(True)
+    got = {n: x.double().cpu().numpy() for n, x in zip(("o", "lse", "dq", "dk", "dv", "dtable"), (o, lse, *grads))}
+    assert c.faults(got, ref) == [] and (got["lse"][0, :, :2] == -np.inf).all()
