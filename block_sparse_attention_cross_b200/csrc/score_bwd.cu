@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if ((F & kBias) && a.table != nullptr && !near) {
         bool bad = false;
         const int n = score_bucket(a, k0 > p0 ? a.R : -a.R, &bad);
-        far = table_entry(__bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n])) * kLog2e;
+        far = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n]) * kLog2e;
         if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
       }
       // The row terms of the first 32 queries are read before the wait for the
@@ -936,8 +936,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const __nv_bfloat16* tab = reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
       n_lo = score_bucket(a, -a.R, &bad);
       n_hi = score_bucket(a, a.R, &bad);
-      far_lo = table_entry(__bfloat162float(tab[n_lo])) * kLog2e;
-      far_hi = table_entry(__bfloat162float(tab[n_hi])) * kLog2e;
+      far_lo = __bfloat162float(tab[n_lo]) * kLog2e;
+      far_hi = __bfloat162float(tab[n_hi]) * kLog2e;
       if (bad) report_status(a.status, CALIBATT_E_CORRUPT);
     }
     // What key tile k0 adds to this thread's 64 columns' scores (`near`: from window wt & 1).

@@ -56,11 +56,6 @@ __device__ __forceinline__ int score_bucket(const ScoreArgs& a, int off, bool* b
   return n;
 }
 
-// A table entry as the scores get it: one below -2^127 (the types' lowest
-// value, as a mask) counts as -inf.  Kept finite it would absorb the scores,
-// and a row that sees nothing else would have an LSE without its logarithm.
-__device__ __forceinline__ float table_entry(float x) { return x < -0x1p127f ? -INFINITY : x; }
-
 template <int V>
 using IntC = std::integral_constant<int, V>;
 
@@ -221,7 +216,8 @@ __device__ __forceinline__ bool is_near(const ScoreArgs& a, int k0, int p0, int 
   return a.table != nullptr && k0 - p1 < a.R && k0 + 127 - p0 > -a.R;
 }
 
-// Warp-collective; `heads` windows of consecutive heads from h0 on, 256 floats apart (log2 units).
+// Warp-collective; `heads` windows of consecutive heads from h0 on, 256 floats apart (log2 units: an entry below
+// -2.35e38, as the type's lowest value, becomes -inf).
 __device__ __forceinline__ void fill_window(const ScoreArgs& a, int h0, int heads, int o0, float* win, uint8_t* bwin,
                                             WindowInfo* info, bool* bad) {
   const int lane = lane_id();
@@ -251,7 +247,7 @@ __device__ __forceinline__ void fill_window(const ScoreArgs& a, int h0, int head
     const __nv_bfloat16* tab =
         reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h0 + g) * a.n_buckets;
 #pragma unroll
-    for (int x = 0; x < 8; ++x) win[g * 256 + x * 32 + lane] = table_entry(__bfloat162float(tab[n[x]])) * kLog2e;
+    for (int x = 0; x < 8; ++x) win[g * 256 + x * 32 + lane] = __bfloat162float(tab[n[x]]) * kLog2e;
   }
   if (bwin != nullptr) {
 #pragma unroll

@@ -483,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
       float far_lo = 0.f, far_hi = 0.f;
       if ((F & kBias) && a.table != nullptr) {
-        far_lo = table_entry(__bfloat162float(tab[score_bucket(a, -a.R, &corrupt)])) * kLog2e;
-        far_hi = table_entry(__bfloat162float(tab[score_bucket(a, a.R, &corrupt)])) * kLog2e;
+        far_lo = __bfloat162float(tab[score_bucket(a, -a.R, &corrupt)]) * kLog2e;
+        far_hi = __bfloat162float(tab[score_bucket(a, a.R, &corrupt)]) * kLog2e;
       }
       float m = F & kBounded ? 0.25f * terms.capA : -INFINITY, l = 0.f;
       float best = F & kBounded ? 0.f : -INFINITY;   // kBounded: largest probability; else largest score

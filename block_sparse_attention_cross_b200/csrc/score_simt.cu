@@ -138,7 +138,12 @@ __device__ __forceinline__ void fill_window(const ScoreArgs& a, int h, int o0, W
   if (x < 2 * BT - 1) {
     const int n = score_bucket(a, o0 + x, bad);
     w->bucket[x] = n;
-    w->value[x] = table_entry(reinterpret_cast<const float*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n]);
+    // An entry that log2(e) takes below fp32's range (the lowest value, as a
+    // mask) is -inf, as in the kernels that work in log2 units.  Kept finite it
+    // would absorb the scores, and a row that sees nothing else would have an
+    // LSE without its logarithm.
+    const float v = reinterpret_cast<const float*>(a.table)[static_cast<size_t>(h) * a.n_buckets + n];
+    w->value[x] = v * kLog2e == -INFINITY ? -INFINITY : v;
   }
 }
 

@@ -643,8 +643,8 @@ typedef struct calibatt_score {
   const float* slopes;    /* [H] float32 device or NULL.  A row with a slope other than 0 whose interval reaches
                              farther than 2^24 from its position becomes NaN (fp32 does not hold such distances)
                              and is reported to dev_status by the forward as CALIBATT_E_UNSUPPORTED             */
-  const void* table;      /* [H, n_buckets] of the inputs' type, device, or NULL; an entry below -2^127 counts
-                             as -inf and hides its bucket's keys                                                */
+  const void* table;      /* [H, n_buckets] of the inputs' type, device, or NULL; an entry below -2.35e38 (the
+                             types' lowest values) counts as -inf and hides its bucket's keys                   */
   const int32_t* buckets; /* [2 max_distance + 1] device: bucket of every clipped offset j - p; NULL without a
                              table.  An entry outside [0, n_buckets) is read as bucket 0 and reported to
                              dev_status as CALIBATT_E_CORRUPT                                                   */
