@@ -60,6 +60,11 @@ class AttnSpans:
         return s
 
 
+def _int32(x):
+    """``x`` as the C interface's int: ctypes would wrap a wider one into range, clamped it is refused there."""
+    return max(-(1 << 31), min(int(x), (1 << 31) - 1))
+
+
 def _ints(name, x, shape, device):
     """int32 CUDA tensor of ``shape`` (None: not given); lists and host tensors are copied to the device."""
     if x is None:
@@ -71,8 +76,11 @@ def _ints(name, x, shape, device):
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.is_cuda and t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if t.dtype == torch.int64:   # lengths are clamped on the device; a wrapped value would not be
-        t = t.clamp(-(1 << 31), (1 << 31) - 1)
+    if t.dtype in (torch.int64, torch.uint32, torch.uint64):   # lengths are clamped on the device; a wrapped value would not be
+        w = t.to(torch.int64)
+        if t.dtype == torch.uint64:
+            w = w.masked_fill(w < 0, 1 << 31)
+        t = w.clamp(-(1 << 31), (1 << 31) - 1)
     return t.to(device=device, dtype=torch.int32).contiguous()
 
 
@@ -91,6 +99,8 @@ def attn_spans(B, Nq, Nk, *, causal=False, docs=None, prefix=None, kv_len=None, 
     B, Nq, Nk = int(B), int(Nq), int(Nk)
     if B <= 0 or Nq <= 0 or Nk <= 0:
         raise ValueError("B, Nq and Nk must be positive")
+    if max(B, Nq, Nk) >= 1 << 31:
+        raise ValueError("B, Nq and Nk must be below 2^31")
     device = torch.device(device)
     if device.type != "cuda":
         raise ValueError("the spans are computed on a CUDA device")
@@ -125,9 +135,9 @@ def attn_spans(B, Nq, Nk, *, causal=False, docs=None, prefix=None, kv_len=None, 
 def relative_buckets(n_buckets, max_distance, bidirectional=True, device="cuda"):
     """Bucket map [2 max_distance + 1] int32 of a learned relative bias (``calibatt_relative_buckets``):
     own buckets near zero, logarithmic ones out to ``max_distance``, farther offsets in the last."""
-    n = max(int(max_distance), 0)
+    n = int(max_distance) if 0 < int(max_distance) <= 1 << 20 else 0   # (others are refused before anything is written)
     out = np.zeros(2 * n + 1, dtype=np.int32)
-    check(load().calibatt_relative_buckets(int(n_buckets), int(max_distance), int(bool(bidirectional)),
+    check(load().calibatt_relative_buckets(_int32(n_buckets), _int32(max_distance), int(bool(bidirectional)),
                                            out.ctypes.data_as(ctypes.c_void_p)))
     return torch.from_numpy(out).to(device)
 
@@ -188,12 +198,12 @@ def _prepare(q, k, v, spans, scale, cap, slopes, table, buckets, mask, map_offse
         _flat("table", table, (H, table.shape[1]), q.dtype, dev)
         _flat("buckets", buckets, tuple(buckets.shape), torch.int32, dev)
         sc.table, sc.buckets = table.data_ptr(), buckets.data_ptr()
-        sc.n_buckets, sc.max_distance = table.shape[1], buckets.numel() // 2
+        sc.n_buckets, sc.max_distance = _int32(table.shape[1]), _int32(buckets.numel() // 2)
     if mask is not None:
         if mask.dim() != 3:
             raise ValueError("mask must be uint8 [n_maps, nqb, nkb]")
         _flat("mask", mask, (mask.shape[0], -(-Nq // 128), -(-Nk // 128)), torch.uint8, dev)
-        sc.mask, sc.n_maps, sc.map_offset = mask.data_ptr(), mask.shape[0], int(map_offset)
+        sc.mask, sc.n_maps, sc.map_offset = mask.data_ptr(), mask.shape[0], _int32(map_offset)
     if status is not None:
         if status.dtype != torch.int32 or status.numel() < 1:
             raise ValueError("status must be an int32 tensor with at least one element")
@@ -278,7 +288,7 @@ def score_attn_bwd(dout, q, k, v, o, lse, spans: AttnSpans, *, scale=None, cap=0
     outs = [_tensor4("dq", dq, qs, dt, dev), _tensor4("dk", dk, ks, dt, dev), _tensor4("dv", dv, ks, dt, dev)]
     dtable = None if table is None else torch.empty_like(table)
     sizes = (B, H, Hkv, Nq, Nk, d, _DTYPES[dt])
-    nbytes = _bwd_bytes(*sizes, 0 if table is None else table.shape[1])
+    nbytes = _bwd_bytes(*sizes, 0 if table is None else _int32(table.shape[1]))
     ws = _workspace(nbytes, dev)
     ref = ctypes.byref
     sp = spans.as_struct()

@@ -137,3 +137,11 @@ def test_lowest_table_values_hide_keys(dtype, kw, low, Nq, Nk):
     ref = c.reference(True)
     got = {n: x.double().cpu().numpy() for n, x in zip(("o", "lse", "dq", "dk", "dv", "dtable"), (o, lse, *grads))}
     assert c.faults(got, ref) == [] and (got["lse"][0, :, :2] == -np.inf).all()
+
+
+def test_map_offset_beyond_int_is_refused():
+    q = torch.zeros(1, 2, 130, 64, dtype=BF, device="cuda")
+    mask = torch.ones(4, 2, 2, dtype=torch.uint8, device="cuda")
+    for off in (1 << 32, (1 << 32) + 2, -(1 << 32)):
+        with pytest.raises(cba.CalibattError, match="map_offset"):
+            cba.score_attn_fwd(q, q, q, cba.attn_spans(1, 130, 130), mask=mask, map_offset=off)
