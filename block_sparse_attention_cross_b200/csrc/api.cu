@@ -79,36 +79,44 @@ void load_encode() {
       q == cudaDriverEntryPointSuccess)
     g_encode = reinterpret_cast<EncodeTiledFn>(fn);
 }
-}  // namespace
 
-int make_tmap_bf16(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+// bf16, 128-byte swizzle, zero fill.  The encoder is a driver call and needs a
+// current context, which a host thread whose first CUDA work this is does not
+// have yet: the runtime binds the current device's, and the call is repeated.
+int encode_map(CUtensorMap* tm, uint32_t rank, void* base, const cuuint64_t* dims, const cuuint64_t* strides,
+               const cuuint32_t* box) {
   std::call_once(g_encode_once, load_encode);
   if (g_encode == nullptr) return set_error(CALIBATT_E_CUDA, "cuTensorMapEncodeTiled is unavailable");
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols * 2};
-  const cuuint32_t box[2] = {64, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-                              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = CUDA_SUCCESS;
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, base, dims, strides, box, estr,
+                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_ERROR_INVALID_CONTEXT && r != CUDA_ERROR_NOT_INITIALIZED) break;
+    int dev = 0;
+    if (int rc = current_device(&dev)) return rc;
+    if (cudaSetDevice(dev) != cudaSuccess) return check_launch("cudaSetDevice");
+  }
   if (r != CUDA_SUCCESS) return set_error(CALIBATT_E_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
   return CALIBATT_OK;
 }
+}  // namespace
+
+int make_tmap_bf16(CUtensorMap* tm, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {cols * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  return encode_map(tm, 2, const_cast<void*>(base), dims, strides, box);
+}
 
 int make_tmap4_bf16(CUtensorMap* tm, const Tensor4& t, int B, int heads, int N, int d, int box_n, int box_h) {
-  std::call_once(g_encode_once, load_encode);
-  if (g_encode == nullptr) return set_error(CALIBATT_E_CUDA, "cuTensorMapEncodeTiled is unavailable");
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(heads),
                               static_cast<cuuint64_t>(B)};
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(t.sn) * 2, static_cast<cuuint64_t>(t.sh) * 2,
                                  static_cast<cuuint64_t>(t.sb) * 2};
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_n), static_cast<cuuint32_t>(box_h), 1};
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUresult r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t.p, dims, strides, box, estr,
-                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) return set_error(CALIBATT_E_CUDA, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
-  return CALIBATT_OK;
+  return encode_map(tm, 4, t.p, dims, strides, box);
 }
 
 int configure_kernel(const void* kern, std::atomic<bool>* done, size_t smem, int regs, const char* what) {
