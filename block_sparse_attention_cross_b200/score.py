@@ -142,19 +142,24 @@ def relative_buckets(n_buckets, max_distance, bidirectional=True, device="cuda")
     return torch.from_numpy(out).to(device)
 
 
+def _strides_fit(t):
+    """Whether a [B, heads, N, d] tensor has strides that ``calibatt_tensor4`` takes."""
+    sb, sh, sn, sd = t.stride()
+    step = 16 // t.element_size()
+    return not (sd != 1 or (t.shape[0] > 1 and (sb <= 0 or sb % step)) or (t.shape[1] > 1 and (sh <= 0 or sh % step))
+                or (t.shape[2] > 1 and (sn <= 0 or sn % step)))
+
+
 def _tensor4(name, t, shape, dtype, device):
     """Checks a [B, heads, N, d] tensor and returns its ``calibatt_tensor4``."""
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    sb, sh, sn, sd = t.stride()
-    step = 16 // t.element_size()
-    if (sd != 1 or (shape[0] > 1 and (sb <= 0 or sb % step)) or (shape[1] > 1 and (sh <= 0 or sh % step))
-            or (shape[2] > 1 and (sn <= 0 or sn % step))):
+    if not _strides_fit(t):
         raise ValueError(f"{name}: the last dimension must be contiguous and the others' strides positive multiples "
                          f"of 16 bytes, got strides {t.stride()} (an expanded tensor needs .contiguous())")
-    return _lib.Tensor4(t.data_ptr(), sb, sh, sn)
+    return _lib.Tensor4(t.data_ptr(), *t.stride()[:3])
 
 
 def _flat(name, t, shape, dtype, device):
@@ -244,7 +249,19 @@ def score_attn_fwd(q, k, v, spans: AttnSpans, *, scale=None, cap=0.0, slopes=Non
     :func:`relative_buckets`).  ``mask``: uint8 [n_maps, nqb, nkb] kept 128 x
     128 blocks (as :func:`calibrate` returns), head h uses map ``map_offset``
     + h.  Returns O (laid out like q) and, with ``return_lse``, LSE [B, H, Nq].
+
+    With gradients enabled and an input that requires one, O is part of the
+    graph: its backward is :func:`score_attn_bwd`, for q, k, v and the table.
+    (With ``out`` the returned tensor is, ``out`` itself stays outside.)  The
+    LSE and the slopes have no gradient; a backward that asks for one raises.
     """
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
+                                    or (table is not None and table.requires_grad)
+                                    or (slopes is not None and slopes.requires_grad)):
+        o, lse = _ScoreAttention.apply(q, k, v, table, slopes, spans, out, lse,
+                                       dict(scale=scale, cap=cap, buckets=buckets, mask=mask, map_offset=map_offset,
+                                            status=status))
+        return (o, lse) if return_lse else o
     (B, H, Hkv, Nq, Nk, d), sc = _prepare(q, k, v, spans, scale, cap, slopes, table, buckets, mask, map_offset, status)
     dev, dt = q.device, q.dtype
     tq = _tensor4("q", q, (B, H, Nq, d), dt, dev)
@@ -296,3 +313,37 @@ def score_attn_bwd(dout, q, k, v, o, lse, spans: AttnSpans, *, scale=None, cap=0
         *map(ref, ins), _ptr(lse), *map(ref, outs), _ptr(dtable), *sizes, ref(sp), ref(sc), _ptr(ws), nbytes,
         _ptr(status), _stream(dev))))
     return (dq, dk, dv) if table is None else (dq, dk, dv, dtable)
+
+
+class _ScoreAttention(torch.autograd.Function):
+    """:func:`score_attn_fwd` as a node of the graph."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, table, slopes, spans, out, lse, kw):
+        # The caller's buffers enter as aliases: marked as written, so that an
+        # older graph that saved them notices, but without a history of their
+        # own, which would chain the graphs of calls that share them.
+        given = [t for t in (out, lse) if t is not None]
+        out, lse = (None if t is None else t.detach() for t in (out, lse))
+        o, lse = score_attn_fwd(q, k, v, spans, table=table, slopes=slopes, out=out, lse=lse, return_lse=True, **kw)
+        torch.autograd.graph.increment_version(given)
+        ctx.save_for_backward(q, k, v, table, slopes, o, lse)
+        ctx.spans, ctx.kw = spans, kw
+        ctx.set_materialize_grads(False)
+        return o, lse
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout, dlse):
+        if dlse is not None:
+            raise RuntimeError("the LSE of score_attn_fwd has no gradient: use it detached")
+        if ctx.needs_input_grad[4]:
+            raise RuntimeError("the slopes of score_attn_fwd have no gradient: pass them detached")
+        if dout is None:
+            return (None,) * 9
+        q, k, v, table, slopes, o, lse = ctx.saved_tensors
+        if not _strides_fit(dout) or dout.data_ptr() % 16:   # (a sum's gradient is expanded)
+            dout = dout.contiguous()
+        grads = score_attn_bwd(dout, q, k, v, o, lse, ctx.spans, table=table, slopes=slopes, **ctx.kw)
+        dq, dk, dv = (g if need else None for g, need in zip(grads[:3], ctx.needs_input_grad))
+        return dq, dk, dv, grads[3] if ctx.needs_input_grad[3] else None, None, None, None, None, None
