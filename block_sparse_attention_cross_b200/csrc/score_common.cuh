@@ -24,7 +24,8 @@ __device__ __forceinline__ int2 score_row(const ScoreArgs& a, int b, int i) {
 // Whether the row at position p sees a key farther away than fp32 counts.
 // Positions go up to 2^30, and with rounded distances neighbouring keys would
 // get the same one, or jump by many: with a slope such a row becomes NaN
-// (through a NaN slope) and is reported.
+// (through its sum, which costs the walk over the keys nothing) and is
+// reported.
 constexpr int kMaxSlopeDistance = 1 << 24;
 __device__ __forceinline__ bool score_far(int2 vis, int p) {
   return vis.x < vis.y && max(abs(vis.x - p), abs(vis.y - 1 - p)) > kMaxSlopeDistance;

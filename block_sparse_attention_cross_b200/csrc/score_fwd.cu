@@ -474,11 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int p0 = a.q_start[w.b] + (a.packed ? 0 : w.qb * TILE);   // positions of the tile's rows: p0 ... p1
       const int p1 = p0 + (a.packed ? a.Nq : TILE) - 1;
       const int p = a.q_start[w.b] + i;
-      float slope = a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
-      if ((F & kBias) && slope != 0.f && score_far(vis, p)) {
-        slope = NAN;
-        report_status(a.status, CALIBATT_E_UNSUPPORTED);
-      }
+      const float slope = a.slopes != nullptr ? a.slopes[h] * kLog2e : 0.f;
       const __nv_bfloat16* tab =
           reinterpret_cast<const __nv_bfloat16*>(a.table) + static_cast<size_t>(h) * a.n_buckets;
       float far_lo = 0.f, far_hi = 0.f;
@@ -735,6 +731,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++tiles;
       tc_fence_after();
       see_bad(gb);
+      if ((F & kBias) && slope != 0.f && l != 0.f && score_far(vis, p)) {
+        l = NAN;
+        report_status(a.status, CALIBATT_E_UNSUPPORTED);
+      }
       const float inv_l = row_bad ? NAN : l == 0.f ? 0.f : 1.f / (l + corr);
       const float row_lse = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
       if (a.parts > 1) {

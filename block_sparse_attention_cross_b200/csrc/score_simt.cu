@@ -179,8 +179,9 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
   const int qb = q0 >> 7;
   const int4 t = score_tile(a, b, qb);
   const int qs = a.q_start[b];
+  const float slope = a.slopes != nullptr ? a.slopes[h] : 0.f;
   int2 vis[4];
-  float m[4], l[4], slope[4], o[4][D / 16];
+  float m[4], l[4], o[4][D / 16];
   bool nan_row[4], bad = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -188,11 +189,6 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
     m[i] = -INFINITY;
     l[i] = 0.f;
     nan_row[i] = false;
-    slope[i] = a.slopes != nullptr ? a.slopes[h] : 0.f;
-    if (slope[i] != 0.f && score_far(vis[i], qs + q0 + ty * 4 + i)) {
-      slope[i] = NAN;
-      report_status(a.status, CALIBATT_E_UNSUPPORTED);
-    }
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
   }
@@ -220,7 +216,7 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
         const int col = k0 + tx + 16 * j;
         float th;
         const bool see = col >= vis[i].x && col < vis[i].y;
-        s[i][j] = see ? score_of(a, slope[i], win, s[i][j], ty * 4 + i, tx + 16 * j, col - (qs + q0 + ty * 4 + i), &th)
+        s[i][j] = see ? score_of(a, slope, win, s[i][j], ty * 4 + i, tx + 16 * j, col - (qs + q0 + ty * 4 + i), &th)
                       : -INFINITY;
         if (edge && see && bad_row[tx + 16 * j]) nan_row[i] = true;
         mx = fmaxf(mx, s[i][j]);
@@ -253,6 +249,10 @@ __global__ void __launch_bounds__(kThreads) k_score_fwd_simt(const ScoreArgs a) 
     const unsigned any = __ballot_sync(0xffffffffu, nan_row[i]) >> (threadIdx.x & 16);
     const int r = q0 + ty * 4 + i;
     if (r >= a.Nq) continue;
+    if (slope != 0.f && l[i] != 0.f && score_far(vis[i], qs + r)) {
+      l[i] = NAN;
+      report_status(a.status, CALIBATT_E_UNSUPPORTED);
+    }
     const float inv = (any & 0xffffu) ? NAN : l[i] == 0.f ? 0.f : 1.f / l[i];
     const float row_lse = l[i] == 0.f ? -INFINITY : m[i] + logf(l[i]);
     const size_t at = (static_cast<size_t>(b) * a.H + h) * a.Nq + r;

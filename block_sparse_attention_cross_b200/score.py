@@ -142,24 +142,19 @@ def relative_buckets(n_buckets, max_distance, bidirectional=True, device="cuda")
     return torch.from_numpy(out).to(device)
 
 
-def _strides_fit(t):
-    """Whether a [B, heads, N, d] tensor has strides that ``calibatt_tensor4`` takes."""
-    sb, sh, sn, sd = t.stride()
-    step = 16 // t.element_size()
-    return not (sd != 1 or (t.shape[0] > 1 and (sb <= 0 or sb % step)) or (t.shape[1] > 1 and (sh <= 0 or sh % step))
-                or (t.shape[2] > 1 and (sn <= 0 or sn % step)))
-
-
 def _tensor4(name, t, shape, dtype, device):
     """Checks a [B, heads, N, d] tensor and returns its ``calibatt_tensor4``."""
     if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} of shape {shape}, got {t.dtype} of shape {tuple(t.shape)}")
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor on {device}")
-    if not _strides_fit(t):
+    sb, sh, sn, sd = t.stride()
+    step = 16 // t.element_size()
+    if (sd != 1 or (shape[0] > 1 and (sb <= 0 or sb % step)) or (shape[1] > 1 and (sh <= 0 or sh % step))
+            or (shape[2] > 1 and (sn <= 0 or sn % step))):
         raise ValueError(f"{name}: the last dimension must be contiguous and the others' strides positive multiples "
                          f"of 16 bytes, got strides {t.stride()} (an expanded tensor needs .contiguous())")
-    return _lib.Tensor4(t.data_ptr(), *t.stride()[:3])
+    return _lib.Tensor4(t.data_ptr(), sb, sh, sn)
 
 
 def _flat(name, t, shape, dtype, device):
@@ -342,8 +337,12 @@ class _ScoreAttention(torch.autograd.Function):
         if dout is None:
             return (None,) * 9
         q, k, v, table, slopes, o, lse = ctx.saved_tensors
-        if not _strides_fit(dout) or dout.data_ptr() % 16:   # (a sum's gradient is expanded)
+        try:
+            _tensor4("dout", dout, q.shape, q.dtype, q.device)
+        except ValueError:   # strides that the kernels do not take (a sum's gradient is expanded)
             dout = dout.contiguous()
+        if dout.data_ptr() % 16:
+            dout = dout.clone()
         grads = score_attn_bwd(dout, q, k, v, o, lse, ctx.spans, table=table, slopes=slopes, **ctx.kw)
         dq, dk, dv = (g if need else None for g, need in zip(grads[:3], ctx.needs_input_grad))
         return dq, dk, dv, grads[3] if ctx.needs_input_grad[3] else None, None, None, None, None, None
