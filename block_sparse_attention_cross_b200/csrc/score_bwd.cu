@@ -650,20 +650,22 @@ __device__ __forceinline__ void add_to_bucket(float* acc, float v) {
 
 // dZ of 32 columns whose offsets meet boundaries k ... k1 - 1 of a window:
 // column x is entry `entry` + x.  Per segment the row's sum, added up over the
-// warp.
+// warp.  (Each segment from its own columns: as a difference of running sums a
+// small bucket behind a large one kept only the large one's rounding.)
 __device__ __forceinline__ void sum_by_cuts(const uint32_t (&g)[32], const WindowInfo& info, int k, int k1, int entry,
                                          float* acc) {
-  float before = 0.f;
+  int from = 0;
   for (; k <= k1; ++k) {
-    const int cut = k < k1 ? info.at[k] - entry : 32;
+    const int cut = k < k1 ? min(max(info.at[k] - entry, from), 32) : 32;
+    const unsigned len = cut - from;
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
     for (int x = 0; x < 32; x += 2) {
-      if (x < cut) s0 += u2f(g[x]);
-      if (x + 1 < cut) s1 += u2f(g[x + 1]);
+      if (static_cast<unsigned>(x - from) < len) s0 += u2f(g[x]);
+      if (static_cast<unsigned>(x + 1 - from) < len) s1 += u2f(g[x + 1]);
     }
-    add_to_bucket(acc + info.bucket[k], s0 + s1 - before);
-    before = s0 + s1;
+    add_to_bucket(acc + info.bucket[k], s0 + s1);
+    from = cut;
   }
 }
 

@@ -145,3 +145,19 @@ def test_map_offset_beyond_int_is_refused():
     for off in (1 << 32, (1 << 32) + 2, -(1 << 32)):
         with pytest.raises(cba.CalibattError, match="map_offset"):
             cba.score_attn_fwd(q, q, q, cba.attn_spans(1, 130, 130), mask=mask, map_offset=off)
+
+
+# steep slopes: buckets whose gradient is far below their neighbours' keep their own digits
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("kw", [
+    dict(H=5, Hkv=1, Nq=108, Nk=759, cap=50.0, buckets=64, distance=79, docs=[[45, 225, 263, 612, 697]], q_start=[434], seed=633140, steep=4),
+    dict(H=5, Hkv=1, Nq=108, Nk=759, cap=50.0, buckets=64, distance=79, docs=[[45, 225, 263, 612, 697]], q_start=[434], seed=633140, steep=-1),
+    dict(H=2, Nq=200, buckets=8, distance=400, steep=4), dict(H=2, Nq=200, buckets=8, distance=400, steep=-8, causal=True),
+    dict(H=4, Nq=300, buckets=16, distance=60, steep=16), dict(H=2, Nq=300, d=128, buckets=32, distance=120, causal=True, steep=8),
+])
+def test_small_buckets_beside_large_ones(dtype, kw):
+    kw = dict(kw)
+    steep = kw.pop("steep", 1)
+    c = Narrow(dtype=dtype, slopes=True, **kw)
+    c.slopes = c.slopes * steep
+    c.verify()
