@@ -32,8 +32,8 @@
 // sweep at least, against 1024 (first sweep), 1536 and 2048 (dK/dV) tensor
 // cycles at d = 128.  24 heads of 8192 tokens, d = 128: dQ 1.71 ms, dK/dV 1.30
 // ms, together 0.5 PFLOP/s of the products that the gradients need and 0.9 of
-// those that run; with a cap 2.29 and 1.77.  The tensor pipe is 38% busy
-// (capped), the issue slots 40%; the rest is the latency of dependent
+// those that run; with a cap 2.18 and 1.68.  The tensor pipe is 38% busy
+// (capped), the issue slots 43%; the rest is the latency of dependent
 // instructions (1.8 stalled warps an issue).
 #include <algorithm>
 #include <atomic>

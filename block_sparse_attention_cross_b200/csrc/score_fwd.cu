@@ -33,7 +33,7 @@
 // alone on its sub-partition, runs at its latencies: 2300 cycles of softmax a
 // pair for plain scores, 3300 capped or with slopes, 5100 with both, beside
 // 1660 of products.  24 heads of 8192 tokens, d = 128: 0.91 ms plain (907
-// TFLOP/s), 1.14 capped, 1.13 with slopes, 1.04 with a table.  (Two warpgroups
+// TFLOP/s), 1.14 capped, 1.13 with slopes, 1.06 with a table.  (Two warpgroups
 // a slot, half of the columns each: capped 1.10, but plain 0.96, a table 1.30
 // ms.)  Few queries: HBM; 4 tokens of 24 heads read 930 MB of K and V in 0.15
 // ms (6.2 TB/s, 96% of the measured copy), 32 sequences of different lengths
@@ -834,6 +834,8 @@ bool score_packs(int G, int Nq, bool mask, bool table) {
 // out sequences of different lengths, lose more than they win: 4 tokens, 24
 // heads, 75 600 keys 150 us in one round, 165 in two, 180 in four; 32
 // sequences of 2500 ... 8191 keys 162, 174, 160; 8 of 4800 ... 16 000 76, 70, 82.
+// Only equal splits were compared, not ones in proportion to the lengths, and
+// 149 to 296 units get one split whatever slots that leaves idle.
 int score_splits(int B, int heads, int nq_tiles, int nkb) {
   const long long tiles = static_cast<long long>(B) * heads * nq_tiles;
   return static_cast<int>(std::max<long long>(1, std::min<long long>(296 / tiles, nkb / 2)));

@@ -725,6 +725,9 @@ int calibatt_score_attn_fwd(const calibatt_tensor4* q, const calibatt_tensor4* k
  *             calibatt_score_attn_bwd_workspace_size bytes (n_buckets: 0
  *             without dtable).
  * Every gradient is summed in a fixed order without atomics: deterministic.
+ * P is exp(z - LSE) of float32 numbers: its relative error grows with the LSE
+ * as 2^-22 |LSE_i| (1% where every key of a row is 40 000 away under a slope
+ * of 1).
  * The sums are float32 (the table's partial sums are joined in float64);
  * CALIBATT_BF16 rounds P and dS to bf16 for their products.  Asynchronous.
  * Errors: as calibatt_score_attn_fwd.
