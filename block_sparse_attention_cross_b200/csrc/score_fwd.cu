@@ -55,7 +55,8 @@ static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs == kThreads * kLaunchR
 constexpr int kProducer0 = 8, kMma = 9, kWindow = 10, kProducer1 = 11;
 constexpr uint32_t kTmemCols = 512;
 // The reference maximum is raised, and O rescaled, only when a tile's maximum
-// exceeds it by more than this many log2 units: P stays below 2^64.
+// exceeds it by more than this many log2 units: P stays below 2^64, and sums
+// over 2^24 keys inside fp32 for |v| < 2^39.
 constexpr float kRescaleThreshold = 64.0f;
 constexpr int kMaxPackedTable = 4;   // heads of a packed tile with a table (windows in shared memory, two buffers)
 

@@ -697,7 +697,8 @@ int calibatt_relative_buckets(int n_buckets, int max_distance, int bidirectional
  *  q, o  [B, H, Nq, d];  k, v  [B, Hkv, Nk, d] of `dtype`;  lse [B, H, Nq]
  *  float32 or NULL.  H a multiple of Hkv; d in {64, 128}; CALIBATT_BF16
  *  (tcgen05 tensor cores, fp32 accumulation, probabilities rounded to bf16
- *  for the second product) or CALIBATT_FP32 (FFMA).
+ *  for the second product; |v| below 2^39, larger values may leave fp32's
+ *  range in the sums) or CALIBATT_FP32 (FFMA).
  *  workspace  device, 256-byte aligned, of at least
  *             calibatt_score_attn_fwd_workspace_size bytes (0: may be NULL).
  * Few query rows against many keys are split along the keys and joined by a
